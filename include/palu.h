@@ -290,6 +290,166 @@ palu_status palu_decode_attn_noalloc(const palu_config* cfg, int batch, const vo
                                      const void* B_v, void* out, float* lse, int num_splits,
                                      palu_stream_t stream, int32_t* status_out);
 
+/* ---- Planning a step, sparse decode over selected pages, verification ------
+ * "PALU 论文低秩投影分解" §在 serving 里的直接收益 (the compressed cache combines
+ * with paged KV and continuous batching): these calls keep the page bookkeeping
+ * of a serving step on the GPU, let a step of a long context read only the pages
+ * that can matter to its queries, and check the drafted tokens whose queries a
+ * multi-token step scored.  The pages name none of them; their definitions are
+ * this library's.
+ * Workspaces of these calls hold counters: zero-fill a workspace once before
+ * its first use and keep it to one of the calls (of any sizes it is large enough
+ * for); every call leaves its counters back at zero.  Calls that overlap on the
+ * GPU need workspaces of their own.  The current device must be
+ * the one that owns `stream` and the pointers. */
+
+/* Append plan: pages, slots and positions of the tokens a step appends.
+ *   num_new    [batch] int32        tokens sequence b appends; negative: it drops
+ *                                   its last -num_new[b] tokens (rejected drafts,
+ *                                   or all of them when the request is finished)
+ *   seq_lens   [batch] int32        cached tokens; updated
+ *   page_table [batch][max_pages] int32  updated: pages got are entered, entries
+ *                                   of pages given back become -1, others stay
+ *   free_pages [num_pages] int32    stack of unused pages, its top at index
+ *                                   num_free - 1; updated
+ *   num_free   [1] int32            updated
+ *   slot_mapping, positions [n_rows] int32 (written): rows of the appended
+ *              tokens, sequence after sequence in index order.  Row r of
+ *              sequence b, r - row_starts[b] = j: position seq_lens[b] + j (its
+ *              length before the call), slot page·page_size + offset as
+ *              palu_compress_append takes it.  Rows of a sequence that got no
+ *              pages and rows past the last sequence: slot -1, position 0.
+ *   row_starts [batch + 1] int32 or NULL (written): Σ_{b'<b} max(num_new[b'], 0)
+ *   taken      [batch] int32 or NULL (written): num_new[b], or 0 where refused
+ * Pages come off the top of the stack in (sequence, page) order.  A sequence
+ * gets all the pages it needs or none: it is refused (its length and table stay)
+ * when the needs of the sequences up to it exceed num_free.  Pages given back
+ * go on top of what is left, the last in (sequence, page) order first, so
+ * dropping what the last call appended restores the stack; they serve the next
+ * call, not this one.
+ * Refused and reported as PALU_ERR_DEVICE_BOUNDS: a length that would leave
+ * [0, max_pages·page_size], or rows past n_rows.  Also reported: a num_free
+ * outside [0, num_pages] (taken as 0) and page numbers outside the pool (their
+ * rows get slot -1).
+ * batch <= PALU_PLAN_MAX_BATCH (PALU_ERR_UNSUPPORTED above); page_size a multiple
+ * of 8; num_pages·page_size below 2^31.  One launch, no synchronisation. */
+#define PALU_PLAN_MAX_BATCH 8192
+palu_status palu_plan_workspace_size(int batch, size_t* bytes);
+palu_status palu_plan_append(int page_size, int batch, int max_pages, int num_pages, int n_rows,
+                             const int32_t* num_new, int32_t* seq_lens, int32_t* page_table,
+                             int32_t* free_pages, int32_t* num_free, int32_t* slot_mapping,
+                             int32_t* positions, int32_t* row_starts, int32_t* taken, void* workspace,
+                             size_t workspace_bytes, palu_stream_t stream);
+
+/* Verification of drafted tokens against the target's probabilities, with the
+ * random numbers given: the accepted tokens are distributed as if the target
+ * had sampled them one by one.
+ *   dtype        F32, F16 or BF16: the type of both probability arrays
+ *   target_probs [batch][num_drafts + 1][vocab], rows target_ld elements apart
+ *   draft_probs  [batch][num_drafts][vocab], rows draft_ld elements apart, or
+ *                NULL: each draft was certain (probability 1 on itself)
+ *   draft_tokens [batch][num_drafts] int32
+ *   draft_lens   [batch] int32 in [0, num_drafts] or NULL: all num_drafts
+ *   u_accept     [batch][num_drafts] float32, u_sample [batch] float32, in [0, 1)
+ * Draft i of sequence b, x its token, is accepted when every draft before it was
+ * and u_accept[b][i]·q(x) < p(x) (compared without rounding).  With a drafts
+ * accepted, the next token is the least v whose running sum of weights exceeds
+ * u_sample[b] times their total; the weights are max(p - q, 0) of row a where
+ * draft a was refused, p of row a where all were accepted, and p where every
+ * max(p - q, 0) is zero.  Differences and sums are taken in float64.  A weight
+ * that is not a finite positive number counts as zero.
+ *   tokens       [batch][num_drafts + 1] int32 (written): the accepted drafts,
+ *                the sampled token (-1 where no weight is positive), then -1
+ *   num_accepted [batch] int32 (written)
+ *   rollback     [batch] int32 or NULL (written): num_accepted - draft_lens[b],
+ *                what palu_plan_append takes to drop the refused drafts
+ * A draft token outside [0, vocab) is refused, a draft_lens outside its range is
+ * clamped; both are reported as PALU_ERR_DEVICE_BOUNDS.
+ * 0 <= num_drafts <= PALU_MAX_DRAFTS, batch <= PALU_VERIFY_MAX_BATCH and vocab <=
+ * 2^28 (PALU_ERR_UNSUPPORTED above). */
+#define PALU_MAX_DRAFTS 32
+#define PALU_VERIFY_MAX_BATCH 8192
+palu_status palu_verify_workspace_size(int batch, int num_drafts, int vocab, size_t* bytes);
+palu_status palu_verify_drafts(int dtype, int batch, int num_drafts, int vocab, const void* target_probs,
+                               long long target_ld, const void* draft_probs, long long draft_ld,
+                               const int32_t* draft_tokens, const int32_t* draft_lens, const float* u_accept,
+                               const float* u_sample, int32_t* tokens, int32_t* num_accepted,
+                               int32_t* rollback, void* workspace, size_t workspace_bytes,
+                               palu_stream_t stream);
+
+/* Bounds pool: for every (page, group) and channel c of the group's width W the
+ * least and the largest rebuilt, rotated key entry over the page's cached tokens,
+ *   bounds [num_pages][G][2][W] act dtype: [0] the least, [1] the largest,
+ *   k_t = R(pos_t)(z_k,t · B_k), R as in palu_decode_attn,
+ * rounded outwards (down, up) into F16 / BF16, so that q'·k_t never exceeds
+ * Σ_c max(q'_c lo_c, q'_c hi_c) by more than float32 rounding.  A key entry that is
+ * not a number is left out; a channel with no entry at all gets (+inf, -inf). */
+palu_status palu_page_bounds_bytes(const palu_config* cfg, size_t* bytes_per_page);
+
+/* Rebuild the bounds of the pages that hold tokens first[b] .. seq_lens[b] - 1 of
+ * every sequence (first NULL: all of its pages), each from all its cached
+ * tokens: after an append, first[b] is the first appended token; after dropping
+ * tokens, the sequence's new length (its last page shrank).  Pages past the
+ * sequence and pages before first[b] stay as they are.
+ *   first [batch] int32 or NULL; ranks_k [G] HOST int32 or NULL (per-group key
+ *   ranks, as in the ranked calls); the rest as in palu_decode_attn. */
+palu_status palu_page_bounds_workspace_size(const palu_config* cfg, int batch, int max_pages, size_t* bytes);
+palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int batch, const int32_t* first,
+                             const void* zk_pool, const void* zk_scales, const int32_t* pos_pool,
+                             const int32_t* page_table, int max_pages, const int32_t* seq_lens, int num_pages,
+                             const void* B_k, void* bounds, void* workspace, size_t workspace_bytes,
+                             palu_stream_t stream);
+
+/* Page selection: for every query and head group the list_len pages of largest
+ *   score(page) = max over the group's heads h of Σ_c max(q'_h,c lo_c, q'_h,c hi_c),
+ * q' = R(q_pos) q: an upper bound, times √d_h, of every score the page holds.
+ *   q          [batch][num_queries][H][head_dim], q_pos [batch][num_queries]
+ *   pos_pool   the cache's position pool or NULL
+ *   num_first, num_last   pages always kept: the first num_first and the last
+ *              num_last of those the query sees; num_first + num_last <= list_len
+ *   page_list  [batch][num_queries][G][list_len] int32 (written): logical pages,
+ *              ascending, then -1
+ *   page_counts [batch][num_queries][G] int32 (written): min(list_len, pages seen)
+ *   page_scores [batch][num_queries][G][list_len] float32 or NULL (written): the
+ *              listed pages' scores, -inf behind them
+ * A query sees every page of its sequence; with num_queries > 1 and no position
+ * pool only those that hold a token at or before q_pos.  Scores are computed in
+ * float64; of equal scores the lower page wins; a head's sum that is not a number
+ * counts as -inf.  batch·G <= PALU_SELECT_MAX_LISTS (PALU_ERR_UNSUPPORTED above). */
+#define PALU_SELECT_MAX_LISTS 65536
+palu_status palu_select_workspace_size(const palu_config* cfg, int batch, int num_queries, int max_pages,
+                                       size_t* bytes);
+palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries, const void* q,
+                              const int32_t* q_pos, const void* bounds, const int32_t* pos_pool,
+                              const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                              int num_pages, int num_first, int num_last, int list_len, int32_t* page_list,
+                              int32_t* page_counts, float* page_scores, void* workspace,
+                              size_t workspace_bytes, palu_stream_t stream);
+
+/* Decode step over listed pages only: palu_decode_attn (num_queries = 1) or
+ * palu_decode_attn_multi (num_queries > 1, causal by position) where query j of
+ * sequence b attends, in head group g, to the cached tokens of the logical pages
+ * page_list[b][j][g][0 .. page_counts[b][j][g]) instead of all.
+ *   page_list   [batch][num_queries][G][list_len] int32, strictly ascending
+ *   page_counts [batch][num_queries][G] int32 in [0, list_len]; 0: out = 0, lse = -inf
+ * A list that is not ascending or names a page past the sequence is reported as
+ * PALU_ERR_DEVICE_BOUNDS (the result is void).  The softmax weights reach the
+ * value product as the sum of two 16-bit numbers, so F16 / BF16 results carry
+ * float32 accuracy up to the final rounding.  num_splits (0 = automatic) splits
+ * the lists; ranks_k / ranks_v as in the ranked calls.
+ * batch·num_queries <= 65535 (PALU_ERR_UNSUPPORTED above). */
+palu_status palu_decode_pages_workspace_size(const palu_config* cfg, const int32_t* ranks_k,
+                                             const int32_t* ranks_v, int batch, int num_queries, int list_len,
+                                             int num_splits, size_t* bytes);
+palu_status palu_decode_attn_pages(const palu_config* cfg, const int32_t* ranks_k, const int32_t* ranks_v,
+                                   int batch, int num_queries, const void* q, const int32_t* q_pos,
+                                   const void* zk_pool, const void* zv_pool, const void* zk_scales,
+                                   const void* zv_scales, const int32_t* pos_pool, const int32_t* page_table,
+                                   int max_pages, const int32_t* seq_lens, const int32_t* page_list,
+                                   const int32_t* page_counts, int list_len, int num_pages, const void* B_k,
+                                   const void* B_v, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int num_splits, palu_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device status word at the
  * start of `workspace`.  Returns PALU_OK, PALU_ERR_DEVICE_TIMEOUT or
  * PALU_ERR_DEVICE_BOUNDS; *detail (optional) receives the kernel's detail code. */

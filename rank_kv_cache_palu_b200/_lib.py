@@ -68,6 +68,28 @@ SIGNATURES = {
                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
                                         c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_size_t, c_int, c_void_p]),
+    "palu_plan_workspace_size": (c_int, [c_int, _P(c_size_t)]),
+    "palu_plan_append": (c_int, [c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                 c_void_p]),
+    "palu_verify_workspace_size": (c_int, [c_int, c_int, c_int, _P(c_size_t)]),
+    "palu_verify_drafts": (c_int, [c_int, c_int, c_int, c_int, c_void_p, ctypes.c_longlong, c_void_p,
+                                   ctypes.c_longlong, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_size_t, c_void_p]),
+    "palu_page_bounds_bytes": (c_int, [_CFG, _P(c_size_t)]),
+    "palu_page_bounds_workspace_size": (c_int, [_CFG, c_int, c_int, _P(c_size_t)]),
+    "palu_page_bounds": (c_int, [_CFG, _P(c_int32), c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                 c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "palu_select_workspace_size": (c_int, [_CFG, c_int, c_int, c_int, _P(c_size_t)]),
+    "palu_select_pages": (c_int, [_CFG, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                  c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_size_t, c_void_p]),
+    "palu_decode_pages_workspace_size": (c_int, [_CFG, _P(c_int32), _P(c_int32), c_int, c_int, c_int, c_int,
+                                                 _P(c_size_t)]),
+    "palu_decode_attn_pages": (c_int, [_CFG, _P(c_int32), _P(c_int32), c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                       c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_size_t, c_int, c_void_p]),
     "palu_get_device_status": (c_int, [c_void_p, c_void_p, _P(c_int32)]),
     "palu_status_string": (ctypes.c_char_p, [c_int]),
     "palu_last_cuda_error": (ctypes.c_char_p, []),

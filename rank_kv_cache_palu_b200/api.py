@@ -248,6 +248,234 @@ def palu_decode_attn_noalloc(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_sca
     _check(st, "palu_decode_attn_noalloc")
 
 
+# ---------------------------------------------------------------- planning, sparse steps, verification
+# These calls check shapes and element types of every tensor, take the device from the tensors (it
+# need not be the current one) and, without a stream, run on that device's current stream.
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
+class _Args:
+    """Checks the tensors of one call and gives their addresses."""
+
+    __slots__ = ("where", "device")
+
+    def __init__(self, where: str):
+        self.where = where
+        self.device = None
+
+    def __call__(self, name, t, dtype, shape=None):
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.where}: {name} must be a torch.Tensor or None")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{self.where}: {name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{self.where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.where}: {name} must be contiguous")
+        return self.address(name, t)
+
+    def address(self, name, t):
+        if t.numel() == 0:
+            return None
+        if not t.is_cuda:
+            raise ValueError(f"{self.where}: {name} must live in CUDA device memory")
+        d = t.device.index
+        if self.device is None:
+            self.device = d
+        elif self.device != d:
+            raise ValueError(f"{self.where}: {name} is on cuda:{d}, other tensors are on cuda:{self.device}")
+        return t.data_ptr()
+
+    def rows(self, name, t, dtype, shape):
+        """Address and row stride of [batch][rows][width] probabilities; rows may be padded."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.where}: {name} must be a torch.Tensor")
+        if t.dtype is not dtype:
+            raise ValueError(f"{self.where}: {name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{self.where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        b, n, width = shape
+        sb, ld, se = t.stride()
+        ld = ld if n > 1 else sb if b > 1 else width          # a dimension of one has no stride to keep to
+        if (width > 1 and se != 1) or (b > 1 and sb != n * ld) or ld < width:
+            raise ValueError(f"{self.where}: rows of {name} must be contiguous and evenly spaced")
+        return self.address(name, t), ld
+
+    def call(self, fn, *args, stream=None):
+        if self.device is None or self.device == torch.cuda.current_device():
+            _check(fn(*args, _stream(stream)), self.where)
+            return
+        with torch.cuda.device(self.device):
+            _check(fn(*args, _stream(stream)), self.where)
+
+
+def _size(where: str, *args) -> int:
+    out = ctypes.c_size_t()
+    _check(getattr(load(), where)(*args, ctypes.byref(out)), where)
+    return int(out.value)
+
+
+def palu_plan_workspace_size(batch: int) -> int:
+    return _size("palu_plan_workspace_size", batch)
+
+
+def palu_plan_append(page_size: int, num_new, seq_lens, page_table, free_pages, num_free, slot_mapping, positions,
+                     row_starts, taken, workspace, stream=None):
+    """Pages, slots and positions of the tokens every sequence appends (or drops: negative num_new).
+
+    num_new, seq_lens [batch], page_table [batch][max_pages], free_pages [num_pages] (a stack of
+    num_free[0] unused pages), slot_mapping and positions [n_rows]; seq_lens, page_table, free_pages
+    and num_free are updated.  row_starts [batch + 1] and taken [batch] may be None.
+    """
+    A = _Args("palu_plan_append")
+    batch, max_pages = page_table.shape
+    one = (batch,)
+    A.call(load().palu_plan_append, page_size, batch, max_pages, free_pages.numel(), slot_mapping.numel(),
+           A("num_new", num_new, _I32, one), A("seq_lens", seq_lens, _I32, one), A("page_table", page_table, _I32),
+           A("free_pages", free_pages, _I32, (free_pages.numel(),)), A("num_free", num_free, _I32, (1,)),
+           A("slot_mapping", slot_mapping, _I32, (slot_mapping.numel(),)),
+           A("positions", positions, _I32, (slot_mapping.numel(),)),
+           A("row_starts", row_starts, _I32, (batch + 1,)), A("taken", taken, _I32, one),
+           A("workspace", workspace, None), workspace.numel() * workspace.element_size(), stream=stream)
+
+
+_PROBS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def palu_verify_workspace_size(batch: int, num_drafts: int, vocab: int) -> int:
+    return _size("palu_verify_workspace_size", batch, num_drafts, vocab)
+
+
+def palu_verify_drafts(target_probs, draft_probs, draft_tokens, draft_lens, u_accept, u_sample, tokens, num_accepted,
+                       rollback, workspace, stream=None):
+    """Accept drafts against the target's probabilities and draw the token after them.
+
+    target_probs [batch][D + 1][V], draft_probs [batch][D][V] or None (certain drafts), both float32,
+    float16 or bfloat16 with evenly spaced rows (a slice of padded rows will do); draft_tokens and
+    u_accept [batch][D], draft_lens [batch] or None, u_sample [batch]; tokens [batch][D + 1],
+    num_accepted and rollback (or None) [batch] are written.
+    """
+    A = _Args("palu_verify_drafts")
+    batch, n, vocab = target_probs.shape
+    if target_probs.dtype not in _PROBS:
+        raise ValueError(f"palu_verify_drafts: probabilities must be float32, float16 or bfloat16, "
+                         f"got {target_probs.dtype}")
+    one, D = (batch,), n - 1
+    p, p_ld = A.rows("target_probs", target_probs, target_probs.dtype, (batch, n, vocab))
+    q, q_ld = (None, 0) if draft_probs is None or D == 0 else \
+        A.rows("draft_probs", draft_probs, target_probs.dtype, (batch, D, vocab))
+    A.call(load().palu_verify_drafts, _PROBS[target_probs.dtype], batch, D, vocab, p, p_ld, q, q_ld,
+           A("draft_tokens", draft_tokens, _I32, (batch, D)), A("draft_lens", draft_lens, _I32, one),
+           A("u_accept", u_accept, _F32, (batch, D)), A("u_sample", u_sample, _F32, one),
+           A("tokens", tokens, _I32, (batch, n)), A("num_accepted", num_accepted, _I32, one),
+           A("rollback", rollback, _I32, one), A("workspace", workspace, None),
+           workspace.numel() * workspace.element_size(), stream=stream)
+
+
+def _act(cfg: PaluConfig):
+    return _ACT_TORCH[cfg.act_dtype]
+
+
+_ACT_TORCH = {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
+
+
+def _bounds_numel(cfg: PaluConfig, num_pages: int) -> int:
+    return num_pages * 2 * cfg.num_heads * cfg.head_dim
+
+
+def palu_page_bounds_bytes(cfg: PaluConfig) -> int:
+    """Bytes of one page of the bounds pool [num_pages][G][2][group width], act dtype."""
+    return _size("palu_page_bounds_bytes", ctypes.byref(cfg))
+
+
+def palu_page_bounds_workspace_size(cfg: PaluConfig, batch: int, max_pages: int) -> int:
+    return _size("palu_page_bounds_workspace_size", ctypes.byref(cfg), batch, max_pages)
+
+
+def _pool(A, name, pool, num_pages, page_bytes):
+    """A cache pool that holds at least num_pages pages."""
+    if pool is not None and pool.numel() * pool.element_size() < num_pages * page_bytes:
+        raise ValueError(f"{A.where}: {name} holds fewer than {num_pages} pages")
+    return A(name, pool, None)
+
+
+def palu_page_bounds(cfg: PaluConfig, first, zk_pool, zk_scales, pos_pool, page_table, seq_lens, num_pages: int, B_k,
+                     bounds, workspace, ranks_k=None, stream=None):
+    """Rebuild the key bounds of the pages holding tokens first[b] .. seq_lens[b] - 1 (first None: all)."""
+    A = _Args("palu_page_bounds")
+    batch, max_pages = page_table.shape
+    if bounds.numel() < _bounds_numel(cfg, num_pages):
+        raise ValueError(f"palu_page_bounds: bounds holds fewer than {num_pages} pages")
+    kb, _, ksb, _ = palu_cache_strides(cfg) if ranks_k is None else \
+        palu_cache_strides_ranked(cfg, ranks_k, ranks_k)[:4]
+    A.call(load().palu_page_bounds, ctypes.byref(cfg), _ranks(ranks_k), batch, A("first", first, _I32, (batch,)),
+           _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
+           _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size), A("page_table", page_table, _I32), max_pages,
+           A("seq_lens", seq_lens, _I32, (batch,)), num_pages, A("B_k", B_k, _act(cfg)),
+           A("bounds", bounds, _act(cfg)), A("workspace", workspace, None),
+           workspace.numel() * workspace.element_size(), stream=stream)
+
+
+def palu_select_workspace_size(cfg: PaluConfig, batch: int, num_queries: int, max_pages: int) -> int:
+    return _size("palu_select_workspace_size", ctypes.byref(cfg), batch, num_queries, max_pages)
+
+
+def palu_select_pages(cfg: PaluConfig, q, q_pos, bounds, pos_pool, page_table, seq_lens, num_pages: int,
+                      num_first: int, num_last: int, page_list, page_counts, page_scores, workspace, stream=None):
+    """The pages of largest score bound for every query and head group.
+
+    q [batch][Q][H][d_h], q_pos [batch][Q]; page_list [batch][Q][G][list_len] (ascending, then -1),
+    page_counts [batch][Q][G] and page_scores (like page_list, or None) are written.
+    """
+    A = _Args("palu_select_pages")
+    batch, Q = q_pos.shape
+    G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
+    if bounds.numel() < _bounds_numel(cfg, num_pages):
+        raise ValueError(f"palu_select_pages: bounds holds fewer than {num_pages} pages")
+    A.call(load().palu_select_pages, ctypes.byref(cfg), batch, Q,
+           A("q", q, _act(cfg), (batch, Q, cfg.num_heads, cfg.head_dim)), A("q_pos", q_pos, _I32),
+           A("bounds", bounds, _act(cfg)), A("pos_pool", pos_pool, _I32),
+           A("page_table", page_table, _I32, (batch, max_pages)), max_pages, A("seq_lens", seq_lens, _I32, (batch,)),
+           num_pages, num_first, num_last, keep, A("page_list", page_list, _I32, (batch, Q, G, keep)),
+           A("page_counts", page_counts, _I32, (batch, Q, G)),
+           A("page_scores", page_scores, _F32, (batch, Q, G, keep)), A("workspace", workspace, None),
+           workspace.numel() * workspace.element_size(), stream=stream)
+
+
+def palu_decode_pages_workspace_size(cfg: PaluConfig, batch: int, num_queries: int, list_len: int,
+                                     num_splits: int = 0, ranks_k=None, ranks_v=None) -> int:
+    return _size("palu_decode_pages_workspace_size", ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch,
+                 num_queries, list_len, num_splits)
+
+
+def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scales, zv_scales, pos_pool, page_table,
+                           seq_lens, page_list, page_counts, num_pages: int, B_k, B_v, out, lse, workspace,
+                           num_splits: int = 0, ranks_k=None, ranks_v=None, stream=None):
+    """Decode step over listed pages: query j of sequence b attends, in group g, to the tokens of the
+    logical pages page_list[b][j][g][:page_counts[b][j][g]] (strictly ascending).
+
+    q and out [batch][Q][H][d_h], q_pos [batch][Q], lse [batch][Q][H] or None; Q > 1 is causal by position.
+    """
+    A = _Args("palu_decode_attn_pages")
+    batch, Q = q_pos.shape
+    G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
+    rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _act(cfg)
+    kb, vb, ksb, vsb = palu_cache_strides(cfg) if ranks_k is None else \
+        palu_cache_strides_ranked(cfg, ranks_k, ranks_v)[:4]
+    A.call(load().palu_decode_attn_pages, ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch, Q,
+           A("q", q, act, rows), A("q_pos", q_pos, _I32), _pool(A, "zk_pool", zk_pool, num_pages, kb),
+           _pool(A, "zv_pool", zv_pool, num_pages, vb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
+           _pool(A, "zv_scales", zv_scales, num_pages, vsb),
+           _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size),
+           A("page_table", page_table, _I32, (batch, max_pages)), max_pages, A("seq_lens", seq_lens, _I32, (batch,)),
+           A("page_list", page_list, _I32, (batch, Q, G, keep)), A("page_counts", page_counts, _I32, (batch, Q, G)),
+           keep, num_pages, A("B_k", B_k, act), A("B_v", B_v, act), A("out", out, act, rows),
+           A("lse", lse, _F32, rows[:3]), A("workspace", workspace, None),
+           workspace.numel() * workspace.element_size(), num_splits, stream=stream)
+
+
 def palu_get_device_status(workspace, stream=None) -> tuple[int, int]:
     """(status, detail) of the device status word; clears it."""
     detail = ctypes.c_int32()

@@ -29,6 +29,8 @@ int tc_head_blocks(const palu_config* c) { return c->group_size / 2; }
 
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st) {
   if (a.gs % 2 != 0) return cudaErrorInvalidValue;
+  if (a.page_list != nullptr)
+    return a.lat == PALU_INT4 ? launch_decode_pages_tc_int4(a, st) : launch_decode_pages_tc(a, st);
   if (a.lat == PALU_INT4) return launch_decode_tc_int4(a, st);
   if (a.act == PALU_BF16)
     return a.r_v == 256 ? launch_t<PALU_BF16, 2, PALU_BF16>(a, st) : launch_t<PALU_BF16, 1, PALU_BF16>(a, st);

@@ -18,17 +18,17 @@ TraceSetting trace_setting() { return g_trace; }
 static TimeoutTest g_timeout_test{0, 0};
 TimeoutTest timeout_test_setting() { return g_timeout_test; }
 void count_launch(int n) { g_launches.fetch_add((unsigned long long)n, std::memory_order_relaxed); }
-}  // namespace palu
-
-namespace {
-
-thread_local char g_cuda_err[256] = "";
-
+static thread_local char g_cuda_err[256] = "";
 palu_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return PALU_OK;
   snprintf(g_cuda_err, sizeof(g_cuda_err), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
   return PALU_ERR_CUDA;
 }
+}  // namespace palu
+
+namespace {
+
+using palu::cuda_status;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -386,22 +386,37 @@ palu_status compress_layer(const Layer& L, int n_tokens, int d_model, const void
 // set, passes of queries run one after another on the stream, sharing the
 // workspace.  With Q > 1 a query attends only to the tokens at or before its
 // own position.
+//
+// With page lists (list_len > 0) the step is sparse: every query is a sequence of
+// its own to the kernels, so one launch per set serves all queries, each over its
+// own list of pages.
+struct PageLists {
+  const int32_t* list = nullptr;
+  const int32_t* counts = nullptr;
+  int len = 0;
+};
+
 palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const int32_t* q_pos,
                          const void* zk_pool, const void* zv_pool, const void* zk_scales, const void* zv_scales,
                          const int32_t* pos_pool, const int32_t* page_table, int max_pages, const int32_t* seq_lens,
                          int num_pages, const void* B_k, const void* B_v, void* out, float* lse, void* workspace,
-                         size_t workspace_bytes, int num_splits, palu_stream_t stream) {
+                         size_t workspace_bytes, int num_splits, palu_stream_t stream,
+                         const PageLists* sparse = nullptr) {
   const palu_config* cfg = &L.cfg;
   if (batch < 0 || max_pages <= 0 || num_pages < 0 || num_splits < 0 || Q < 1 || Q > kMaxQueries)
     return PALU_ERR_INVALID_ARG;
-  if (num_splits > max_pages) return PALU_ERR_INVALID_ARG;
+  const int walk = sparse ? sparse->len : max_pages;   // pages a query can walk
+  if (num_splits > walk) return PALU_ERR_INVALID_ARG;
+  if (sparse && (long long)batch * Q > 65535) return PALU_ERR_UNSUPPORTED;
   size_t fused_off = 0;
-  const size_t need = decode_workspace(L, batch, Q, max_pages, num_splits, &fused_off);
+  const size_t need = sparse ? decode_workspace(L, batch * Q, 1, walk, num_splits, &fused_off)
+                             : decode_workspace(L, batch, Q, max_pages, num_splits, &fused_off);
   if (workspace == nullptr || workspace_bytes < need) return PALU_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
   if (batch == 0) return PALU_OK;
   if (!q || !q_pos || !zk_pool || !zv_pool || !page_table || !seq_lens || !B_k || !B_v || !out)
     return PALU_ERR_INVALID_ARG;
+  if (sparse && (!sparse->list || !sparse->counts || num_pages == 0)) return PALU_ERR_INVALID_ARG;
   const bool int4 = cfg->latent_dtype == PALU_INT4;
   if (int4 && (!zk_scales || !zv_scales)) return PALU_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(zk_pool) || !aligned16(zv_pool) || !aligned16(B_k) ||
@@ -444,12 +459,23 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
   a.qpos_bstride = Q;
   a.lse_bstride = Q * a.H;
   a.causal = Q > 1;
+  if (sparse) {
+    a.page_list = sparse->list;
+    a.page_counts = sparse->counts;
+    a.list_len = sparse->len;
+    a.queries = Q;
+    a.batch = batch * Q;
+    a.q_bstride = a.o_bstride = qrow;
+    a.qpos_bstride = 1;
+    a.lse_bstride = a.H;
+    Q = 1;                              // one pass: the queries are among the sequences
+  }
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   for (int c = 0; c < L.nset; ++c) {
     const palu_config cc = set_cfg(L, c);
     const int kind = kernel_kind(&cc);
-    a.S = run_S(&cc, kind, batch, max_pages, num_splits, pass_queries(kind, Q));
+    a.S = run_S(&cc, kind, a.batch, walk, num_splits, pass_queries(kind, Q));
     a.r_k = cc.rank_k;
     a.r_v = cc.rank_v;
     a.k_row = palu::latent_row_bytes(a.lat, a.r_k);
@@ -495,7 +521,7 @@ const char* palu_status_string(palu_status s) {
   return "unknown status";
 }
 
-const char* palu_last_cuda_error(void) { return g_cuda_err; }
+const char* palu_last_cuda_error(void) { return palu::g_cuda_err; }
 
 int palu_decode_kernel_kind(const palu_config* cfg) { return kernel_kind(cfg); }
 
@@ -605,6 +631,121 @@ palu_status palu_decode_ranked_workspace_size(const palu_config* cfg, const int3
     return PALU_ERR_INVALID_ARG;
   *bytes = decode_workspace(L, batch, num_queries, max_pages, num_splits, nullptr);
   return PALU_OK;
+}
+
+palu_status palu_decode_pages_workspace_size(const palu_config* cfg, const int32_t* ranks_k, const int32_t* ranks_v,
+                                             int batch, int num_queries, int list_len, int num_splits,
+                                             size_t* bytes) {
+  Layer L;
+  palu_status s = make_layer(cfg, ranks_k, ranks_v, &L);
+  if (s != PALU_OK) return s;
+  if (bytes == nullptr || batch < 0 || list_len <= 0 || num_splits < 0 || num_splits > list_len || num_queries < 1 ||
+      num_queries > kMaxQueries)
+    return PALU_ERR_INVALID_ARG;
+  if ((long long)batch * num_queries > 65535) return PALU_ERR_UNSUPPORTED;
+  *bytes = decode_workspace(L, batch * num_queries, 1, list_len, num_splits, nullptr);
+  return PALU_OK;
+}
+
+palu_status palu_decode_attn_pages(const palu_config* cfg, const int32_t* ranks_k, const int32_t* ranks_v, int batch,
+                                   int num_queries, const void* q, const int32_t* q_pos, const void* zk_pool,
+                                   const void* zv_pool, const void* zk_scales, const void* zv_scales,
+                                   const int32_t* pos_pool, const int32_t* page_table, int max_pages,
+                                   const int32_t* seq_lens, const int32_t* page_list, const int32_t* page_counts,
+                                   int list_len, int num_pages, const void* B_k, const void* B_v, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, int num_splits,
+                                   palu_stream_t stream) {
+  Layer L;
+  palu_status s = make_layer(cfg, ranks_k, ranks_v, &L);
+  if (s != PALU_OK) return s;
+  if (list_len <= 0) return PALU_ERR_INVALID_ARG;
+  PageLists lists;
+  lists.list = page_list;
+  lists.counts = page_counts;
+  lists.len = list_len;
+  return decode_layer(L, batch, num_queries, q, q_pos, zk_pool, zv_pool, zk_scales, zv_scales, pos_pool, page_table,
+                      max_pages, seq_lens, num_pages, B_k, B_v, out, lse, workspace, workspace_bytes, num_splits,
+                      stream, &lists);
+}
+
+palu_status palu_page_bounds_bytes(const palu_config* cfg, size_t* bytes_per_page) {
+  const palu_status s = check_config(cfg);
+  if (s != PALU_OK) return s;
+  if (bytes_per_page == nullptr) return PALU_ERR_INVALID_ARG;
+  *bytes_per_page = (size_t)2 * cfg->num_heads * cfg->head_dim * (cfg->act_dtype == PALU_F32 ? 4 : 2);
+  return PALU_OK;
+}
+
+palu_status palu_page_bounds_workspace_size(const palu_config* cfg, int batch, int max_pages, size_t* bytes) {
+  const palu_status s = check_config(cfg);
+  if (s != PALU_OK) return s;
+  if (bytes == nullptr || batch < 0 || max_pages <= 0) return PALU_ERR_INVALID_ARG;
+  *bytes = kStatusBytes;
+  return PALU_OK;
+}
+
+palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int batch, const int32_t* first,
+                             const void* zk_pool, const void* zk_scales, const int32_t* pos_pool,
+                             const int32_t* page_table, int max_pages, const int32_t* seq_lens, int num_pages,
+                             const void* B_k, void* bounds, void* workspace, size_t workspace_bytes,
+                             palu_stream_t stream) {
+  Layer L;
+  palu_status s = make_layer(cfg, ranks_k, ranks_k, &L);   // the value ranks play no part
+  if (s != PALU_OK) return s;
+  if (batch < 0 || max_pages <= 0 || num_pages < 0) return PALU_ERR_INVALID_ARG;
+  if (batch > 65535) return PALU_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < kStatusBytes) return PALU_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
+  if (batch == 0) return PALU_OK;
+  const bool int4 = cfg->latent_dtype == PALU_INT4;
+  if (!zk_pool || !page_table || !seq_lens || !B_k || !bounds || (int4 && !zk_scales) || num_pages == 0)
+    return PALU_ERR_INVALID_ARG;
+  if (!aligned16(zk_pool) || !aligned16(B_k) || !aligned16(bounds) || (int4 && !aligned16(zk_scales)))
+    return PALU_ERR_ALIGNMENT;
+  palu::GroupMap gm{};
+  build_map(L, nullptr, 0, zk_pool, nullptr, zk_scales, nullptr, gm);
+  uint64_t omega[palu::kMaxHalfDim];
+  fill_omega(cfg, omega);
+  return cuda_status(palu::launch_page_bounds(cfg, gm, L.bk_rows, batch, first, pos_pool, page_table, max_pages,
+                                              seq_lens, num_pages, B_k, bounds, omega, workspace,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+palu_status palu_select_workspace_size(const palu_config* cfg, int batch, int num_queries, int max_pages,
+                                       size_t* bytes) {
+  const palu_status s = check_config(cfg);
+  if (s != PALU_OK) return s;
+  if (bytes == nullptr || batch < 0 || max_pages <= 0 || num_queries < 1 || num_queries > kMaxQueries)
+    return PALU_ERR_INVALID_ARG;
+  *bytes = palu::select_workspace(cfg, batch, num_queries, max_pages);
+  return PALU_OK;
+}
+
+palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries, const void* q, const int32_t* q_pos,
+                              const void* bounds, const int32_t* pos_pool, const int32_t* page_table, int max_pages,
+                              const int32_t* seq_lens, int num_pages, int num_first, int num_last, int list_len,
+                              int32_t* page_list, int32_t* page_counts, float* page_scores, void* workspace,
+                              size_t workspace_bytes, palu_stream_t stream) {
+  const palu_status s = check_config(cfg);
+  if (s != PALU_OK) return s;
+  if (batch < 0 || max_pages <= 0 || num_pages < 0 || num_queries < 1 || num_queries > kMaxQueries || num_first < 0 ||
+      num_last < 0 || list_len <= 0 || (long long)num_first + num_last > list_len)
+    return PALU_ERR_INVALID_ARG;
+  const long long G = cfg->num_heads / cfg->group_size;
+  if (batch * G > PALU_SELECT_MAX_LISTS || batch > 65535 || (long long)cfg->group_size * cfg->head_dim > 16384)
+    return PALU_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < palu::select_workspace(cfg, batch, num_queries, max_pages))
+    return PALU_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
+  if (batch == 0) return PALU_OK;
+  if (!q || !q_pos || !bounds || !page_table || !seq_lens || !page_list || !page_counts) return PALU_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(bounds)) return PALU_ERR_ALIGNMENT;
+  uint64_t omega[palu::kMaxHalfDim];
+  fill_omega(cfg, omega);
+  return cuda_status(palu::launch_select(cfg, batch, num_queries, q, q_pos, bounds, pos_pool != nullptr, page_table,
+                                         max_pages, seq_lens, num_pages, num_first, num_last, list_len, page_list,
+                                         page_counts, page_scores, omega, workspace,
+                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 
 palu_status palu_decode_attn(const palu_config* cfg, int batch, const void* q, const int32_t* q_pos,

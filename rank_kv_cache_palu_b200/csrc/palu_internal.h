@@ -69,6 +69,12 @@ struct DecodeArgs {
   long long wait_cycles;                   // bound of every wait in the tensor-core kernels (SM cycles)
   int stall_test;                          // timeout-path test: the MMA thread first waits on a phase
                                            // that nothing completes, so the launch times out
+  // Sparse steps (palu_decode_attn_pages): every query is a sequence of its own (batch = sequences ×
+  // queries, qn = 1), reading page-table row and length b / queries and only the logical pages
+  // page_list[(b·G + model group)·list_len + i], i < page_counts[b·G + model group].
+  const int32_t* page_list;   // NULL: every page
+  const int32_t* page_counts;
+  int list_len, queries;
 };
 
 // Phase-trace buffer set by palu_debug_trace (NULL: off).
@@ -109,10 +115,32 @@ struct TimeoutTest {
 };
 TimeoutTest timeout_test_setting();
 
+// Logical pages one CTA of a sparse step walks: entries [e0, e1) of its list.
+struct ListRange {
+  const int32_t* list;   // entry e0 of the list
+  int n, T, npg, sb;     // entries, cached tokens, pages and index of the sequence
+  bool ragged_last;      // the last entry is the sequence's partial last page
+};
+
 // CUDA-core kernels (any supported dtype; the only path for float32).
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_compress_simt(const CompressArgs& a, cudaStream_t st);
+
+// Page bounds and page selection (see palu_page_bounds, palu_select_pages).
+cudaError_t launch_page_bounds(const palu_config* c, const GroupMap& gm, int bk_rows, int batch, const int32_t* first,
+                               const int32_t* pos_pool, const int32_t* page_table, int max_pages,
+                               const int32_t* seq_lens, int num_pages, const void* B_k, void* bounds,
+                               const uint64_t* omega, void* workspace, cudaStream_t st);
+size_t select_workspace(const palu_config* c, int batch, int num_queries, int max_pages);
+cudaError_t launch_select(const palu_config* c, int batch, int num_queries, const void* q, const int32_t* q_pos,
+                          const void* bounds, bool explicit_pos, const int32_t* page_table, int max_pages,
+                          const int32_t* seq_lens, int num_pages, int num_first, int num_last, int list_len,
+                          int32_t* page_list, int32_t* page_counts, float* page_scores, const uint64_t* omega,
+                          void* workspace, cudaStream_t st);
+
+// PALU_OK, or PALU_ERR_CUDA with the error's text kept for palu_last_cuda_error.
+palu_status cuda_status(cudaError_t e);
 
 // Counts kernel launches (palu_kernel_launches); call once per launch.
 void count_launch(int n = 1);

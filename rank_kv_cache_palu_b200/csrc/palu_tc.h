@@ -14,6 +14,11 @@ int tc_head_blocks(const palu_config* c);
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t st);
 // The int4-latent instantiations (own translation unit); launch_decode_tc calls it.
 cudaError_t launch_decode_tc_int4(const DecodeArgs& a, cudaStream_t st);
+// The walks over listed pages (DecodeArgs::page_list set; own translation units);
+// launch_decode_tc and launch_decode_fused call them.
+cudaError_t launch_decode_pages_tc(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_decode_pages_tc_int4(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_decode_pages_fused(const DecodeArgs& a, cudaStream_t st);
 
 // Decode without RoPE: the key up-projection folded into the query, scores
 // taken on the cached latents (no key is rebuilt).  Its workspace adds the

@@ -1,0 +1,264 @@
+// Append plan: pages, slots and positions of the tokens a serving step appends,
+// from the sequences' lengths and the stack of free pages.
+//
+// Two prefix sums over the sequences settle everything: Σ max(num_new, 0) gives
+// every sequence its rows, and Σ (pages needed) gives every sequence its place in
+// the free stack (its i-th new page is free_pages[num_free - 1 - before - i]) and,
+// where it exceeds num_free, the refusals.  A row's page then comes from the page
+// table or from the stack; no row depends on another CTA's result.
+//
+// So one launch serves any size: every CTA takes both prefix sums over all
+// sequences for itself (8 bytes a sequence, from L2) and writes its own share of
+// the rows, and the CTA that finishes last (a ticket in the workspace) alone
+// updates what the others have read: lengths, the stack and its count.  Bound by
+// the launch and one chain of dependent loads at serving sizes, by the 8 bytes
+// written per row above.
+#include "palu_common.cuh"
+#include "palu_internal.h"
+
+namespace palu {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowsPerThread = 4;   // grid size: rows a thread is given before another CTA is started
+
+struct PlanArgs {
+  int batch, P, max_pages, num_pages, n_rows;
+  const int32_t* num_new;
+  int32_t* seq_lens;
+  int32_t* page_table;
+  int32_t* free_pages;
+  int32_t* num_free;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* row_starts;
+  int32_t* taken;
+  DevStatus* st;
+  unsigned* ticket;
+};
+
+// Exclusive prefix sum of v over the block; total receives the sum.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long s = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += o;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const long long x = warp_sums[w];
+    if (w < warp) before += x;
+    all += x;
+  }
+  __syncthreads();
+  total = all;
+  return before + s - v;
+}
+
+__device__ __forceinline__ int pages_of(long long tokens, int P) { return (int)((tokens + P - 1) / P); }
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
+  extern __shared__ int32_t smem[];
+  int32_t* start = smem;                  // [batch + 1] first row of each sequence
+  int32_t* len = start + a.batch + 1;     // [batch] length before the call
+  int32_t* take = len + a.batch;          // [batch] tokens appended (0: refused or none) or dropped
+  int32_t* before = take + a.batch;       // [batch] pages taken off the stack by earlier sequences
+  __shared__ long long warp_sums[kWarps];
+  __shared__ int last;
+  const int tid = threadIdx.x;
+
+  const int F0 = *a.num_free;
+  const bool bad_free = F0 < 0 || F0 > a.num_pages;
+  const int F = bad_free ? 0 : F0;
+  if (bad_free && blockIdx.x == 0 && tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 4000000);
+  const long long cap = (long long)a.max_pages * a.P;
+
+  long long rows = 0, through = 0, got = 0, back = 0;   // running totals over the sequences
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    const bool in = b < a.batch;
+    const int L = in ? a.seq_lens[b] : 0;
+    int n = in ? a.num_new[b] : 0;
+    long long total;
+    const long long grow = n > 0 ? n : 0;
+    const long long s0 = rows + block_scan(grow, warp_sums, total);
+    rows += total;
+    const long long left = (long long)L + n;
+    const bool bad = in && (L < 0 || L > cap || left < 0 || left > cap || s0 + grow > a.n_rows);
+    if (bad) {
+      if (blockIdx.x == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 5000000 + b);
+      n = 0;
+    }
+    const int had = bad ? 0 : pages_of(L, a.P);
+    int need = bad || !in ? 0 : pages_of(left, a.P) - had;   // negative: pages given back
+    const long long need_up = need > 0 ? need : 0;
+    const long long p0 = through + block_scan(need_up, warp_sums, total);
+    through += total;
+    if (p0 + need_up > F && need_up > 0) {
+      n = 0;
+      need = 0;
+    }
+    if (need > 0 && p0 + need > got) got = p0 + need;   // admitted sequences come before the first refused
+    if (need < 0) back -= need;
+    if (in) {
+      start[b] = (int)min(s0, (long long)INT32_MAX);
+      len[b] = L;
+      take[b] = n;
+      before[b] = (int)min(p0, (long long)INT32_MAX);
+      if (blockIdx.x == 0) {
+        if (a.row_starts != nullptr) a.row_starts[b] = start[b];
+        if (a.taken != nullptr) a.taken[b] = n;
+      }
+    }
+  }
+  if (tid == 0) {
+    start[a.batch] = (int)min(rows, (long long)INT32_MAX);
+    if (blockIdx.x == 0 && a.row_starts != nullptr) a.row_starts[a.batch] = start[a.batch];
+  }
+  __syncthreads();
+
+  // this CTA's rows
+  const int total_rows = start[a.batch];
+  for (long long r = (long long)blockIdx.x * kThreads + tid; r < a.n_rows; r += (long long)gridDim.x * kThreads) {
+    int slot = -1, pos = 0;
+    if (r < total_rows) {
+      int lo = 0, hi = a.batch - 1;         // the last sequence whose first row is <= r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= r) lo = mid;
+        else hi = mid - 1;
+      }
+      const int b = lo;
+      if (take[b] > 0) {
+        pos = len[b] + (int)(r - start[b]);
+        const int lp = pos / a.P, off = pos - lp * a.P;
+        const int fresh = lp - pages_of(len[b], a.P);   // >= 0: a page taken by this call
+        int32_t* entry = a.page_table + (size_t)b * a.max_pages + lp;
+        const int page = fresh >= 0 ? a.free_pages[F - 1 - before[b] - fresh] : *entry;
+        if (fresh >= 0 && off == 0) *entry = page;      // every new page starts with a new token
+        if (page < 0 || page >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b);
+        else slot = page * a.P + off;
+      }
+    }
+    a.slots[r] = slot;
+    a.positions[r] = pos;
+  }
+
+  // the last CTA to get here updates what every CTA has read
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (tid == 0) *a.ticket = 0;
+  } else {
+    __syncthreads();
+  }
+  // pages got: the largest admitted prefix; pages given back: their sum
+  long long taken_pages = got, given = back;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    taken_pages = max(taken_pages, __shfl_xor_sync(0xffffffffu, taken_pages, off));
+    given += __shfl_xor_sync(0xffffffffu, given, off);
+  }
+  __shared__ long long wmax[kWarps];
+  if ((tid & 31) == 0) {
+    wmax[tid >> 5] = taken_pages;
+    warp_sums[tid >> 5] = given;
+  }
+  __syncthreads();
+  taken_pages = 0;
+  given = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    taken_pages = max(taken_pages, wmax[w]);
+    given += warp_sums[w];
+  }
+  __syncthreads();
+  const long long left = F - taken_pages;     // stack height before the pages given back
+  if (given > 0) {
+    // page j (in (sequence, page) order) of those given back goes to left + given - 1 - j
+    long long done = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      int has = 0, had = 0;
+      if (b < a.batch && take[b] < 0) {
+        had = pages_of(len[b], a.P);
+        has = pages_of((long long)len[b] + take[b], a.P);
+      }
+      long long total;
+      const long long j0 = done + block_scan(had - has, warp_sums, total);
+      done += total;
+      for (int lp = has; lp < had; ++lp) {
+        int32_t* entry = a.page_table + (size_t)b * a.max_pages + lp;
+        const long long at = left + given - 1 - (j0 + lp - has);
+        const int page = *entry;
+        if (page < 0 || page >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b);
+        if (at < a.num_pages) a.free_pages[at] = page;
+        else report(a.st, PALU_ERR_DEVICE_BOUNDS, 4000001);   // more pages given back than the pool has
+        *entry = -1;
+      }
+    }
+  }
+  for (int b = tid; b < a.batch; b += kThreads)
+    if (take[b] != 0) a.seq_lens[b] = len[b] + take[b];
+  if (tid == 0) *a.num_free = (int)min(left + given, (long long)a.num_pages);
+}
+
+size_t smem_bytes(int batch) { return sizeof(int32_t) * (4 * (size_t)batch + 1); }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+}  // namespace palu
+
+extern "C" palu_status palu_plan_workspace_size(int batch, size_t* bytes) {
+  if (bytes == nullptr || batch < 0) return PALU_ERR_INVALID_ARG;
+  *bytes = 512;   // status word, ticket
+  return PALU_OK;
+}
+
+extern "C" palu_status palu_plan_append(int page_size, int batch, int max_pages, int num_pages, int n_rows,
+                                        const int32_t* num_new, int32_t* seq_lens, int32_t* page_table,
+                                        int32_t* free_pages, int32_t* num_free, int32_t* slot_mapping,
+                                        int32_t* positions, int32_t* row_starts, int32_t* taken, void* workspace,
+                                        size_t workspace_bytes, palu_stream_t stream) {
+  if (page_size <= 0 || batch < 0 || max_pages <= 0 || num_pages <= 0 || n_rows < 0) return PALU_ERR_INVALID_ARG;
+  if (page_size % 8 != 0) return PALU_ERR_ALIGNMENT;
+  if (batch > PALU_PLAN_MAX_BATCH || (long long)num_pages * page_size > INT32_MAX ||
+      (long long)max_pages * page_size > INT32_MAX)
+    return PALU_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < 512) return PALU_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
+  if (batch > 0 && (!num_new || !seq_lens || !page_table)) return PALU_ERR_INVALID_ARG;
+  if (!free_pages || !num_free || (n_rows > 0 && (!slot_mapping || !positions))) return PALU_ERR_INVALID_ARG;
+  const void* all[] = {num_new, seq_lens, page_table, free_pages, num_free, slot_mapping, positions, row_starts, taken};
+  for (const void* p : all)
+    if (!palu::aligned4(p)) return PALU_ERR_ALIGNMENT;
+  palu::PlanArgs a{batch, page_size, max_pages, num_pages, n_rows, num_new, seq_lens, page_table, free_pages,
+                   num_free, slot_mapping, positions, row_starts, taken,
+                   static_cast<palu::DevStatus*>(workspace),
+                   reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + 256)};
+  const size_t smem = palu::smem_bytes(batch);
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(palu::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return palu::cuda_status(e);
+  }
+  const long long per = (long long)palu::kThreads * palu::kRowsPerThread;
+  long long grid = ((long long)n_rows + per - 1) / per;
+  grid = grid < 1 ? 1 : grid > 2 * 148 ? 2 * 148 : grid;
+  palu::plan_kernel<<<(int)grid, palu::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  palu::count_launch();
+  return palu::cuda_status(cudaGetLastError());
+}

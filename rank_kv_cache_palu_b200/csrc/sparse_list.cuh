@@ -1,0 +1,50 @@
+// Page lists of the sparse decode step (palu_decode_attn_pages), shared by its
+// tensor-core, fused and CUDA-core kernels.
+#pragma once
+
+#include "palu_common.cuh"
+#include "palu_internal.h"
+
+namespace palu {
+namespace {
+
+// Raw page-table entry of logical page lp; -1 where lp is outside the sequence.
+__device__ __forceinline__ int list_page(const DecodeArgs& a, const ListRange& lr, int lp) {
+  return lp >= 0 && lp < lr.npg ? a.page_table[(size_t)lr.sb * a.max_pages + lp] : -1;
+}
+
+// This CTA's share (split blockIdx.x of a.S) of the list of virtual sequence vb
+// and model group g.  Thread i checks every blockDim-th entry: lists ascend and
+// name pages of the sequence (each page once, the partial last page last).
+__device__ __forceinline__ ListRange list_range(const DecodeArgs& a, int vb, int g, DevStatus* st) {
+  ListRange r;
+  r.sb = vb / a.queries;
+  int T = a.seq_lens[r.sb];
+  const int cap = a.max_pages * a.P;
+  if (T < 0 || T > cap) {
+    if (threadIdx.x == 0) report(st, PALU_ERR_DEVICE_BOUNDS, 1000000 + r.sb);
+    T = T < 0 ? 0 : cap;
+  }
+  r.T = T;
+  r.npg = (T + a.P - 1) / a.P;
+  const size_t li = (size_t)vb * a.G + g;
+  const int32_t* list = a.page_list + li * a.list_len;
+  int n = a.page_counts[li];
+  if (n < 0 || n > a.list_len) {
+    if (threadIdx.x == 0) report(st, PALU_ERR_DEVICE_BOUNDS, 3000000 + vb);
+    n = n < 0 ? 0 : a.list_len;
+  }
+  const int pps = (n + a.S - 1) / a.S;
+  const int e0 = min(n, (int)blockIdx.x * pps), e1 = min(n, e0 + pps);
+  for (int e = e0 + (int)threadIdx.x; e < e1; e += (int)blockDim.x) {
+    const int lp = list[e];
+    if (lp < 0 || lp >= r.npg || (e > 0 && list[e - 1] >= lp)) report(st, PALU_ERR_DEVICE_BOUNDS, 3000000 + vb);
+  }
+  r.list = list + e0;
+  r.n = e1 - e0;
+  r.ragged_last = r.n > 0 && T % a.P != 0 && r.list[r.n - 1] >= r.npg - 1;
+  return r;
+}
+
+}  // namespace
+}  // namespace palu

@@ -1,0 +1,240 @@
+"""palu_decode_attn_pages on the GPU against the CPU oracle, on every decode path.
+
+Error bounds.  A 16-bit result carries its final rounding, half a step: 2^-8 (bf16) or 2^-11 (f16) of
+its value.  Before it, a score is off by at most Σ|q||k|·2^-20 / √d for the hardware sine and cosine,
+twice (query and key) and 4e-5 for |q|, |k| <= 15, so a weight by 8e-5 relative; the weights' split in
+two 16-bit numbers by 2^-16: together 1.2e-4 Σ p|v|.  In float32 angles are correct to 2^-23 and the
+bound is 2e-5 Σ p|v|.  Log-sum-exps are off by at most the score error, 1e-4 (1e-5 in float32).
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as S
+from palu_testlib import build_pools, build_ranked_pools, make_decode_case, make_ranked_case
+from rank_kv_cache_palu_b200 import api as P
+from rank_kv_cache_palu_b200.synth import TORCH_DTYPE, WORKLOADS, normal_tensor
+
+pytestmark = pytest.mark.gpu
+HALF_STEP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+SUM = {"bf16": 1.2e-4, "f16": 1.2e-4, "f32": 2e-5}
+LSE = {"bf16": 1e-4, "f16": 1e-4, "f32": 1e-5}
+
+
+def w7b(**kw):
+    return dataclasses.replace(WORKLOADS["7b_bf16_r256v128_b1_t4k"], num_heads=8, **kw)
+
+
+CASES = {
+    "bf16": (w7b(), 2),
+    "f16_r256": (w7b(act_dtype="f16", latent_dtype="f16", rank_v=256), 2),
+    "two_heads_r64": (w7b(group_size=2, rank_k=64), 2),
+    "norope": (w7b(rope_base=0.0), 3),
+    "norope_f16_r256": (w7b(rope_base=0.0, act_dtype="f16", latent_dtype="f16", rank_v=256), 3),
+    "int4_f16": (dataclasses.replace(WORKLOADS["7b_int4_r256_b8_t32k"], num_heads=8), 2),
+    "int4_bf16": (dataclasses.replace(WORKLOADS["7b_int4_r256_b8_t32k"], num_heads=8, act_dtype="bf16"), 2),
+    "tiny_f32": (WORKLOADS["tiny_f32"], 1),
+    "odd_heads": (dataclasses.replace(WORKLOADS["tiny_f32"], num_heads=6, group_size=3, head_dim=40, act_dtype="bf16",
+                                      latent_dtype="bf16", page_size=24), 1),
+}
+
+
+def pick_lists(case, Q, keep, seed=0, last=True):
+    """Random ascending lists [b][Q][G] of at most `keep` pages."""
+    rng = np.random.default_rng(seed)
+    out = []
+    for t in case.seq_lens:
+        n = -(-t // case.w.page_size)
+        out.append([[sorted(rng.permutation(n)[:min(n, rng.integers(1, keep + 1))].tolist()) if n else []
+                     for _ in range(case.w.groups)] for _ in range(Q)])
+        if last and n:
+            for row in out[-1]:
+                for g in range(0, case.w.groups, 2):
+                    row[g] = sorted(set(row[g][:keep - 1]) | {n - 1})
+    return out
+
+
+def run(case, pools, q, q_pos, lists, keep, num_splits=0, status=0, ranks=(None, None), B=None, table=None, stream=None,
+        lse=True):
+    w, cfg = case.w, case.cfg
+    b, Q = q_pos.shape
+    flat = np.full((b, Q, w.groups, keep), -1, np.int32)
+    counts = np.zeros((b, Q, w.groups), np.int32)
+    for i in range(b):
+        for j in range(Q):
+            for g in range(w.groups):
+                flat[i, j, g, :len(lists[i][j][g])] = lists[i][j][g]
+                counts[i, j, g] = len(lists[i][j][g])
+    out = torch.full((b, Q, w.num_heads, w.head_dim), 9.0, dtype=TORCH_DTYPE[w.act_dtype], device="cuda")
+    ls = torch.full((b, Q, w.num_heads), 9.0, device="cuda") if lse else None
+    ws = torch.zeros(P.palu_decode_pages_workspace_size(cfg, b, Q, keep, num_splits, *ranks), dtype=torch.uint8,
+                     device="cuda")
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    args = (q.cuda(), dev(q_pos), pools["zk"], pools["zv"], pools["zks"], pools["zvs"], pools["pos"],
+            dev(case.page_table if table is None else table), torch.tensor(case.seq_lens, dtype=torch.int32, device="cuda"),
+            dev(flat), dev(counts), case.num_pages, case.B_k.cuda(), case.B_v.cuda(), out, ls, ws)
+    torch.cuda.synchronize()
+    P.palu_decode_attn_pages(cfg, *args, num_splits, *ranks, stream=stream)
+    torch.cuda.synchronize()
+    assert P.palu_get_device_status(ws)[0] == status
+    return out.double().cpu().numpy(), ls.double().cpu().numpy() if lse else None
+
+
+def queries(case, Q, seed=5):
+    w = case.w
+    q = normal_tensor(seed, "q_pages", (len(case.seq_lens), Q, w.num_heads, w.head_dim), w.act_dtype)
+    q_pos = np.array([[int(case.positions(i)[max(T - Q + j, 0)]) if T else j for j in range(Q)]
+                      for i, T in enumerate(case.seq_lens)], np.int32)
+    return q, q_pos
+
+
+def compare(case, out, lse, q, q_pos, lists, inputs):
+    w = case.w
+    b, Q = q_pos.shape
+    for i in range(b):
+        zk, zv, Bk, Bv = inputs(i)
+        for j in range(Q):
+            ref, rl, size = S.decode_attention_pages(q[i, j].double().numpy(), q_pos[i, j], zk, zv, case.positions(i),
+                                                     Bk, Bv, w.group_size, w.rope_base, lists[i][j], w.page_size, Q > 1)
+            off = np.abs(out[i, j] - ref)
+            assert (off <= HALF_STEP[w.act_dtype] * np.abs(ref) + SUM[w.act_dtype] * size + 1e-30).all(), \
+                f"seq {i} query {j}: {off.max():.3e} of {np.abs(ref).max():.3e}"
+            if lse is not None:
+                empty = np.isneginf(rl)
+                assert (np.isneginf(lse[i, j]) == empty).all()
+                np.testing.assert_allclose(lse[i, j][~empty], rl[~empty], rtol=0, atol=LSE[w.act_dtype])
+
+
+def uniform(case):
+    Bk, Bv = case.B_k.double().numpy(), case.B_v.double().numpy()
+    return lambda i: (*case.oracle_latents(i), Bk, Bv)
+
+
+@pytest.mark.parametrize("Q", [1, 3])
+@pytest.mark.parametrize("name", list(CASES))
+def test_listed_pages(name, Q):
+    w, kind = CASES[name]
+    case = make_decode_case(w, [300, 0, 1, 128, 1000])
+    assert P.palu_decode_kernel_kind(case.cfg) == kind
+    q, q_pos = queries(case, Q)
+    pools = build_pools(case)
+    for splits in (0, 1, 3):
+        lists = pick_lists(case, Q, 5, seed=splits)
+        compare(case, *run(case, pools, q, q_pos, lists, 5, splits), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16", "tiny_f32"])
+def test_explicit_positions(name):
+    case = make_decode_case(CASES[name][0], [300, 129, 700], explicit_positions=True)
+    q, q_pos = queries(case, 2)
+    lists = pick_lists(case, 2, 4)
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 4), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16", "odd_heads"])
+def test_every_page_listed_is_the_dense_step(name):
+    case = make_decode_case(CASES[name][0], [515, 77])
+    q, q_pos = queries(case, 1)
+    lists = [[[list(range(-(-t // case.w.page_size)))] * case.w.groups] for t in case.seq_lens]
+    keep = max(len(x[0][0]) for x in lists)
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, keep), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16"])
+def test_long_lists(name):
+    """Lists that wrap every ring and both TMEM slots many times, one split and many."""
+    case = make_decode_case(dataclasses.replace(CASES[name][0], num_heads=4), [40 * 128 - 5])
+    q, q_pos = queries(case, 1)
+    pools = build_pools(case)
+    lists = [[[[p for p in range(40) if p % 5 != 1]]]]
+    for splits in (1, 7, 32):
+        compare(case, *run(case, pools, q, q_pos, lists, 32, splits), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "tiny_f32"])
+def test_queries_that_see_none_of_their_pages(name):
+    case = make_decode_case(CASES[name][0], [600])
+    q, _ = queries(case, 3)
+    q_pos = np.array([[100, 255, 599]], np.int32)
+    lists = [[[[1, 3]] * case.w.groups, [[2]] * case.w.groups, [[0, 4]] * case.w.groups]]
+    if name == "tiny_f32":
+        assert case.w.page_size == 128
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 2), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope"])
+def test_ranks_per_group(name):
+    ranks_k, ranks_v = [128, 256], [128, 256]
+    case = make_ranked_case(CASES[name][0], ranks_k, ranks_v, [300, 700], nq=2)
+    q, q_pos = case.q, case.q_pos
+    lists = [[[[0, 2], [1]], [[0], [0, 2]]], [[[5], [0, 3, 5]], [[1, 2], [4]]]]
+    out, lse = run(case, build_ranked_pools(case), q, q_pos, lists, 3, ranks=(ranks_k, ranks_v))
+    w = case.w
+    for i in range(2):
+        zk, zv, Bk, Bv = case.oracle_inputs(i)
+        for j in range(2):
+            for g in range(2):
+                hs = slice(g * 4, g * 4 + 4)
+                ref, rl, size = S.decode_attention_pages(q[i, j, hs].double().numpy(), q_pos[i, j], zk[g][None],
+                                                         zv[g][None], case.positions(i), Bk[g][None], Bv[g][None], 4,
+                                                         w.rope_base, [lists[i][j][g]], w.page_size, True)
+                off = np.abs(out[i, j, hs] - ref)
+                assert (off <= HALF_STEP[w.act_dtype] * np.abs(ref) + SUM[w.act_dtype] * size).all()
+                np.testing.assert_allclose(lse[i, j, hs], rl, rtol=0, atol=LSE[w.act_dtype])
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16", "tiny_f32"])
+def test_bad_lists_are_reported(name):
+    case = make_decode_case(CASES[name][0], [600])
+    q, q_pos = queries(case, 1)
+    pools = build_pools(case)
+    G = case.w.groups
+    for bad in ([1, 1], [3, 2], [0, 5], [-1, 2]):
+        run(case, pools, q, q_pos, [[[bad] * G]], 2, status=7)
+    table = case.page_table.copy()
+    table[0, 1] = -7
+    run(case, pools, q, q_pos, [[[[1, 2]] * G]], 2, status=7, table=table)
+    good = [[[[0, 4]] * G]]                                  # and the next call is whole again
+    compare(case, *run(case, pools, q, q_pos, good, 2), q, q_pos, good, uniform(case))
+
+
+def test_another_stream_and_no_lse():
+    case = make_decode_case(CASES["bf16"][0], [300, 700])
+    q, q_pos = queries(case, 1)
+    lists = pick_lists(case, 1, 3)
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 3, stream=torch.cuda.Stream(), lse=False), q, q_pos,
+            lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "tiny_f32"])
+def test_rows_behind_the_last_token_are_not_read(name):
+    case = make_decode_case(CASES[name][0], [133, 7])
+    q, q_pos = queries(case, 1)
+    pools = build_pools(case)
+    w = case.w
+    T = TORCH_DTYPE[w.latent_dtype]
+    for pool, rank in (("zk", w.rank_k), ("zv", w.rank_v)):
+        raw = pools[pool].view(case.num_pages, w.groups, rank * T.itemsize // 128, w.page_size, 128)
+        for i, t in enumerate(case.seq_lens):
+            page = int(case.page_table[i, t // w.page_size])
+            junk = raw[page, :, :, t % w.page_size:].contiguous().view(T)
+            junk[..., 0::2], junk[..., 1::2] = float("nan"), float("inf")
+            raw[page, :, :, t % w.page_size:] = junk.view(torch.uint8)
+    lists = [[[[0, 1]] * w.groups], [[[0]] * w.groups]]
+    compare(case, *run(case, pools, q, q_pos, lists, 2), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "int4_f16", "norope"])
+def test_timeout_reports_and_recovers(name):
+    case = make_decode_case(CASES[name][0], [600])
+    q, q_pos = queries(case, 1)
+    pools = build_pools(case)
+    lists = [[[[0, 2, 4]] * case.w.groups]]
+    P.palu_debug_timeout_test(1 << 20, stall=True)
+    try:
+        run(case, pools, q, q_pos, lists, 3, status=6)
+    finally:
+        P.palu_debug_timeout_test()
+    compare(case, *run(case, pools, q, q_pos, lists, 3), q, q_pos, lists, uniform(case))

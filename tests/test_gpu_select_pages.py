@@ -1,0 +1,159 @@
+"""palu_select_pages on the GPU against the CPU oracle: the lists are whole numbers and equal; the
+scores are float64 sums rounded once to float32 (2^-24 relative)."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as S
+from rank_kv_cache_palu_b200 import api as P
+from rank_kv_cache_palu_b200.synth import TORCH_DTYPE, WORKLOADS
+
+pytestmark = pytest.mark.gpu
+PAGE = 128
+W7B = dataclasses.replace(WORKLOADS["7b_bf16_r256v128_b1_t4k"], num_heads=8)
+SHAPES = {
+    "7b_bf16": W7B,
+    "7b_f16": dataclasses.replace(W7B, act_dtype="f16", latent_dtype="f16"),
+    "norope": dataclasses.replace(W7B, rope_base=0.0),
+    "tiny_f32": WORKLOADS["tiny_f32"],
+    "three_heads_d40": dataclasses.replace(W7B, num_heads=6, group_size=3, head_dim=40),
+    "one_head_d8": dataclasses.replace(W7B, num_heads=3, group_size=1, head_dim=8),
+    "d20_f32": dataclasses.replace(WORKLOADS["tiny_f32"], head_dim=20),
+    "twelve_heads": dataclasses.replace(W7B, num_heads=12, group_size=12, head_dim=64),
+}
+
+
+def cfg_of(w):
+    return P.make_config(w.num_heads, w.head_dim, w.group_size, w.rank_k, w.rank_v, w.page_size, w.rope_base,
+                         w.act_dtype, w.latent_dtype)
+
+
+def make(w, lens, Q=1, seed=0, wide=None, levels=None):
+    g = torch.Generator().manual_seed(seed)
+    b, G, W = len(lens), w.groups, w.width
+    wide = wide or max(1, max(-(-t // PAGE) for t in lens))
+    pages = sum(-(-t // PAGE) for t in lens) + 2
+    order = torch.randperm(pages, generator=g).to(torch.int32)
+    table = torch.full((b, wide), -1, dtype=torch.int32)
+    at = 0
+    for i, t in enumerate(lens):
+        n = -(-t // PAGE)
+        table[i, :n] = order[at:at + n]
+        at += n
+    mid, half = torch.randn((pages, G, W), generator=g), torch.rand((pages, G, W), generator=g) + 0.5
+    if levels:                                    # few distinct boxes: many equal scores
+        pick = torch.randint(0, levels, (pages,), generator=g)
+        mid, half = mid[pick], half[pick]
+    bounds = torch.stack([mid - half, mid + half], 2).to(TORCH_DTYPE[w.act_dtype])
+    q = torch.randn((b, Q, w.num_heads, w.head_dim), generator=g).to(TORCH_DTYPE[w.act_dtype])
+    q_pos = torch.tensor([[max(0, t - Q + j) for j in range(Q)] for t in lens], dtype=torch.int32)
+    return dict(w=w, lens=lens, table=table, bounds=bounds, q=q, q_pos=q_pos, pages=pages, pos=None)
+
+
+def run(c, keep, first=1, last=2, status=0, scores=True, ws=None, stream=None):
+    w, cfg = c["w"], cfg_of(c["w"])
+    b, Q = c["q_pos"].shape
+    lists = torch.full((b, Q, w.groups, keep), 99, dtype=torch.int32, device="cuda")
+    counts = torch.full((b, Q, w.groups), 99, dtype=torch.int32, device="cuda")
+    sc = torch.full(lists.shape, 99.0, device="cuda") if scores else None
+    if ws is None:
+        ws = torch.zeros(P.palu_select_workspace_size(cfg, b, Q, c["table"].shape[1]), dtype=torch.uint8, device="cuda")
+    args = [c["q"].cuda(), c["q_pos"].cuda(), c["bounds"].cuda(), None if c["pos"] is None else c["pos"].cuda(),
+            c["table"].cuda(), torch.tensor(c["lens"], dtype=torch.int32, device="cuda")]
+    torch.cuda.synchronize()
+    P.palu_select_pages(cfg, *args, c["pages"], first, last, lists, counts, sc, ws, stream=stream)
+    torch.cuda.synchronize()
+    assert P.palu_get_device_status(ws)[0] == status
+    return lists.cpu().numpy(), counts.cpu().numpy(), sc.cpu().numpy() if scores else None
+
+
+def check(c, keep, first=1, last=2, **kw):
+    w = c["w"]
+    lists, counts, scores = run(c, keep, first, last, **kw)
+    b, Q = c["q_pos"].shape
+    box = c["bounds"].double().numpy()
+    for i, t in enumerate(c["lens"]):
+        for j in range(Q):
+            at = int(c["q_pos"][i, j])
+            seen = t if Q == 1 or c["pos"] is not None else min(t, max(0, at + 1))
+            n = -(-seen // PAGE)
+            mine = box[c["table"][i, :n].numpy()]
+            ref = S.page_scores(c["q"][i, j].double().numpy(), at, mine[:, :, 0], mine[:, :, 1], w.group_size, w.rope_base)
+            for g in range(w.groups):
+                want = S.select_pages(ref[g], keep, first, last) if n else []
+                assert counts[i, j, g] == len(want)
+                assert lists[i, j, g].tolist() == want + [-1] * (keep - len(want)), f"seq {i} query {j} group {g}"
+                if scores is not None:
+                    np.testing.assert_allclose(scores[i, j, g, :len(want)], ref[g][want], rtol=2.0 ** -23)
+                    assert np.isneginf(scores[i, j, g, len(want):]).all()
+
+
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_shapes(name):
+    check(make(SHAPES[name], [5000, 1, 0, 128, 129, 2500]), 9)
+    check(make(SHAPES[name], [1300, 257], Q=3, seed=1), 4)
+
+
+@pytest.mark.parametrize("pages,keep", [(1, 1), (2, 3), (7, 7), (8, 7), (255, 3), (256, 64), (257, 256), (600, 100),
+                                        (1025, 500), (3000, 7)])
+def test_page_counts(pages, keep):
+    w = dataclasses.replace(SHAPES["7b_bf16"], num_heads=2, group_size=1, head_dim=16)
+    check(make(w, [pages * PAGE - 3], seed=pages), keep, 1 if keep > 1 else 0, 1)
+
+
+def test_nothing_forced_and_everything_forced():
+    c = make(SHAPES["7b_bf16"], [3000, 400])
+    check(c, 5, 0, 0)
+    check(c, 5, 5, 0)
+    check(c, 5, 0, 5)
+    check(c, 5, 2, 3)
+    check(c, 40, 20, 20)
+
+
+@pytest.mark.parametrize("levels", [1, 2, 5])
+def test_equal_scores_go_to_the_lower_page(levels):
+    check(make(SHAPES["7b_bf16"], [9000, 700], seed=levels, levels=levels), 13, 1, 1)
+
+
+def test_queries_before_the_last_pages_and_negative_positions():
+    c = make(SHAPES["7b_bf16"], [2000], Q=4)
+    c["q_pos"] = torch.tensor([[-3, 0, 127, 128]], dtype=torch.int32)
+    check(c, 4, 0, 1)
+    c["pos"] = torch.zeros((c["pages"], PAGE), dtype=torch.int32)       # explicit positions: every page is seen
+    check(c, 4, 0, 1)
+
+
+def test_far_positions():
+    c = make(SHAPES["7b_bf16"], [3000])
+    c["q_pos"] = torch.tensor([[2 ** 31 - 1]], dtype=torch.int32)
+    check(c, 6)
+
+
+def test_infinite_and_nan_bounds():
+    c = make(SHAPES["tiny_f32"], [1500], seed=3)
+    c["bounds"][3, :, 1, 0] = float("inf")
+    c["bounds"][4, :, 0, :] = float("nan")
+    c["bounds"][5, 0] = float("nan")
+    check(c, 5, 0, 1, scores=False)
+
+
+def test_bad_pages_and_lengths_are_reported():
+    c = make(SHAPES["7b_bf16"], [1000, 300])
+    c["table"][0, 2] = c["pages"]
+    lists, counts, _ = run(c, 4, status=7)
+    assert 2 not in lists[0]
+    c = make(SHAPES["7b_bf16"], [1000, 300])
+    c["lens"] = [1000, -5]
+    assert run(c, 4, status=7)[1][1].tolist() == [[0] * 2]
+
+
+def test_one_workspace_serves_smaller_calls():
+    ws = torch.zeros(P.palu_select_workspace_size(cfg_of(SHAPES["7b_bf16"]), 3, 2, 60), dtype=torch.uint8, device="cuda")
+    for lens, Q in (([7000, 500, 20], 2), ([900], 1), ([7000, 7000, 7000], 2)):
+        check(make(SHAPES["7b_bf16"], lens, Q=Q, wide=60), 6, ws=ws)
+
+
+def test_another_stream():
+    check(make(SHAPES["7b_bf16"], [7000, 500]), 6, stream=torch.cuda.Stream())
