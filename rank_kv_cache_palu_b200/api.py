@@ -255,17 +255,25 @@ _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
 class _Args:
-    """Checks the tensors of one call and gives their addresses."""
+    """Checks the tensors of one call and gives their addresses.  The workspace names the device."""
 
     __slots__ = ("where", "device")
 
-    def __init__(self, where: str):
+    def __init__(self, where: str, workspace):
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError(f"{where}: workspace must be a torch.Tensor")
         self.where = where
-        self.device = None
+        self.device = workspace.get_device()
 
     def __call__(self, name, t, dtype, shape=None):
         if t is None:
             return None
+        if (isinstance(t, torch.Tensor) and t.get_device() == self.device >= 0 and t.is_contiguous() and
+                (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+        return self._refuse(name, t, dtype, shape)
+
+    def _refuse(self, name, t, dtype, shape):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{self.where}: {name} must be a torch.Tensor or None")
         if dtype is not None and t.dtype is not dtype:
@@ -274,19 +282,14 @@ class _Args:
             raise ValueError(f"{self.where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{self.where}: {name} must be contiguous")
-        return self.address(name, t)
+        return self._elsewhere(name, t)
 
-    def address(self, name, t):
+    def _elsewhere(self, name, t):
         if t.numel() == 0:
             return None
         if not t.is_cuda:
             raise ValueError(f"{self.where}: {name} must live in CUDA device memory")
-        d = t.device.index
-        if self.device is None:
-            self.device = d
-        elif self.device != d:
-            raise ValueError(f"{self.where}: {name} is on cuda:{d}, other tensors are on cuda:{self.device}")
-        return t.data_ptr()
+        raise ValueError(f"{self.where}: {name} is on {t.device}, the workspace on device {self.device}")
 
     def rows(self, name, t, dtype, shape):
         """Address and row stride of [batch][rows][width] probabilities; rows may be padded."""
@@ -301,14 +304,25 @@ class _Args:
         ld = ld if n > 1 else sb if b > 1 else width          # a dimension of one has no stride to keep to
         if (width > 1 and se != 1) or (b > 1 and sb != n * ld) or ld < width:
             raise ValueError(f"{self.where}: rows of {name} must be contiguous and evenly spaced")
-        return self.address(name, t), ld
+        if t.get_device() == self.device >= 0:
+            return t.data_ptr(), ld
+        return self._elsewhere(name, t), ld
 
     def call(self, fn, *args, stream=None):
-        if self.device is None or self.device == torch.cuda.current_device():
-            _check(fn(*args, _stream(stream)), self.where)
-            return
-        with torch.cuda.device(self.device):
-            _check(fn(*args, _stream(stream)), self.where)
+        if self.device < 0:
+            raise ValueError(f"{self.where}: workspace must live in CUDA device memory")
+        if self.device == torch.cuda.current_device():
+            status = fn(*args, self._stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, self._stream(stream))
+        if status != 0:
+            raise PaluError(status, self.where)
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _size(where: str, *args) -> int:
@@ -329,7 +343,7 @@ def palu_plan_append(page_size: int, num_new, seq_lens, page_table, free_pages, 
     num_free[0] unused pages), slot_mapping and positions [n_rows]; seq_lens, page_table, free_pages
     and num_free are updated.  row_starts [batch + 1] and taken [batch] may be None.
     """
-    A = _Args("palu_plan_append")
+    A = _Args("palu_plan_append", workspace)
     batch, max_pages = page_table.shape
     one = (batch,)
     A.call(load().palu_plan_append, page_size, batch, max_pages, free_pages.numel(), slot_mapping.numel(),
@@ -357,7 +371,7 @@ def palu_verify_drafts(target_probs, draft_probs, draft_tokens, draft_lens, u_ac
     u_accept [batch][D], draft_lens [batch] or None, u_sample [batch]; tokens [batch][D + 1],
     num_accepted and rollback (or None) [batch] are written.
     """
-    A = _Args("palu_verify_drafts")
+    A = _Args("palu_verify_drafts", workspace)
     batch, n, vocab = target_probs.shape
     if target_probs.dtype not in _PROBS:
         raise ValueError(f"palu_verify_drafts: probabilities must be float32, float16 or bfloat16, "
@@ -372,10 +386,6 @@ def palu_verify_drafts(target_probs, draft_probs, draft_tokens, draft_lens, u_ac
            A("tokens", tokens, _I32, (batch, n)), A("num_accepted", num_accepted, _I32, one),
            A("rollback", rollback, _I32, one), A("workspace", workspace, None),
            workspace.numel() * workspace.element_size(), stream=stream)
-
-
-def _act(cfg: PaluConfig):
-    return _ACT_TORCH[cfg.act_dtype]
 
 
 _ACT_TORCH = {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
@@ -394,6 +404,20 @@ def palu_page_bounds_workspace_size(cfg: PaluConfig, batch: int, max_pages: int)
     return _size("palu_page_bounds_workspace_size", ctypes.byref(cfg), batch, max_pages)
 
 
+def _page_bytes(cfg: PaluConfig, ranks) -> tuple[int, int]:
+    """Bytes of one page of a latent pool and of its int4 scale pool, for the groups' ranks."""
+    if cfg.latent_dtype != 3:
+        return cfg.page_size * sum(ranks) * (4 if cfg.latent_dtype == 0 else 2), 0
+    return cfg.page_size * sum(ranks) // 2, cfg.page_size * sum((r // 32 * 2 + 15) // 16 * 16 for r in ranks)
+
+
+def _factor(A, name, B, cfg, ranks):
+    """B_k or B_v: the groups' [rank][group width] blocks, back to back."""
+    if B.numel() != sum(ranks) * cfg.group_size * cfg.head_dim:
+        raise ValueError(f"{A.where}: {name} must hold {sum(ranks)} rows of {cfg.group_size * cfg.head_dim}")
+    return A(name, B, _ACT_TORCH[cfg.act_dtype])
+
+
 def _pool(A, name, pool, num_pages, page_bytes):
     """A cache pool that holds at least num_pages pages."""
     if pool is not None and pool.numel() * pool.element_size() < num_pages * page_bytes:
@@ -404,17 +428,17 @@ def _pool(A, name, pool, num_pages, page_bytes):
 def palu_page_bounds(cfg: PaluConfig, first, zk_pool, zk_scales, pos_pool, page_table, seq_lens, num_pages: int, B_k,
                      bounds, workspace, ranks_k=None, stream=None):
     """Rebuild the key bounds of the pages holding tokens first[b] .. seq_lens[b] - 1 (first None: all)."""
-    A = _Args("palu_page_bounds")
+    A = _Args("palu_page_bounds", workspace)
     batch, max_pages = page_table.shape
     if bounds.numel() < _bounds_numel(cfg, num_pages):
         raise ValueError(f"palu_page_bounds: bounds holds fewer than {num_pages} pages")
-    kb, _, ksb, _ = palu_cache_strides(cfg) if ranks_k is None else \
-        palu_cache_strides_ranked(cfg, ranks_k, ranks_k)[:4]
+    rk = ranks_k or (cfg.rank_k,) * (cfg.num_heads // cfg.group_size)
+    kb, ksb = _page_bytes(cfg, rk)
     A.call(load().palu_page_bounds, ctypes.byref(cfg), _ranks(ranks_k), batch, A("first", first, _I32, (batch,)),
            _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
            _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size), A("page_table", page_table, _I32), max_pages,
-           A("seq_lens", seq_lens, _I32, (batch,)), num_pages, A("B_k", B_k, _act(cfg)),
-           A("bounds", bounds, _act(cfg)), A("workspace", workspace, None),
+           A("seq_lens", seq_lens, _I32, (batch,)), num_pages, _factor(A, "B_k", B_k, cfg, rk),
+           A("bounds", bounds, _ACT_TORCH[cfg.act_dtype]), A("workspace", workspace, None),
            workspace.numel() * workspace.element_size(), stream=stream)
 
 
@@ -429,14 +453,14 @@ def palu_select_pages(cfg: PaluConfig, q, q_pos, bounds, pos_pool, page_table, s
     q [batch][Q][H][d_h], q_pos [batch][Q]; page_list [batch][Q][G][list_len] (ascending, then -1),
     page_counts [batch][Q][G] and page_scores (like page_list, or None) are written.
     """
-    A = _Args("palu_select_pages")
+    A = _Args("palu_select_pages", workspace)
     batch, Q = q_pos.shape
     G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
     if bounds.numel() < _bounds_numel(cfg, num_pages):
         raise ValueError(f"palu_select_pages: bounds holds fewer than {num_pages} pages")
     A.call(load().palu_select_pages, ctypes.byref(cfg), batch, Q,
-           A("q", q, _act(cfg), (batch, Q, cfg.num_heads, cfg.head_dim)), A("q_pos", q_pos, _I32),
-           A("bounds", bounds, _act(cfg)), A("pos_pool", pos_pool, _I32),
+           A("q", q, _ACT_TORCH[cfg.act_dtype], (batch, Q, cfg.num_heads, cfg.head_dim)), A("q_pos", q_pos, _I32),
+           A("bounds", bounds, _ACT_TORCH[cfg.act_dtype]), A("pos_pool", pos_pool, _I32),
            A("page_table", page_table, _I32, (batch, max_pages)), max_pages, A("seq_lens", seq_lens, _I32, (batch,)),
            num_pages, num_first, num_last, keep, A("page_list", page_list, _I32, (batch, Q, G, keep)),
            A("page_counts", page_counts, _I32, (batch, Q, G)),
@@ -458,12 +482,12 @@ def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scale
 
     q and out [batch][Q][H][d_h], q_pos [batch][Q], lse [batch][Q][H] or None; Q > 1 is causal by position.
     """
-    A = _Args("palu_decode_attn_pages")
+    A = _Args("palu_decode_attn_pages", workspace)
     batch, Q = q_pos.shape
     G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
-    rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _act(cfg)
-    kb, vb, ksb, vsb = palu_cache_strides(cfg) if ranks_k is None else \
-        palu_cache_strides_ranked(cfg, ranks_k, ranks_v)[:4]
+    rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _ACT_TORCH[cfg.act_dtype]
+    rk, rv = ranks_k or (cfg.rank_k,) * G, ranks_v or (cfg.rank_v,) * G
+    (kb, ksb), (vb, vsb) = _page_bytes(cfg, rk), _page_bytes(cfg, rv)
     A.call(load().palu_decode_attn_pages, ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch, Q,
            A("q", q, act, rows), A("q_pos", q_pos, _I32), _pool(A, "zk_pool", zk_pool, num_pages, kb),
            _pool(A, "zv_pool", zv_pool, num_pages, vb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
@@ -471,7 +495,7 @@ def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scale
            _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size),
            A("page_table", page_table, _I32, (batch, max_pages)), max_pages, A("seq_lens", seq_lens, _I32, (batch,)),
            A("page_list", page_list, _I32, (batch, Q, G, keep)), A("page_counts", page_counts, _I32, (batch, Q, G)),
-           keep, num_pages, A("B_k", B_k, act), A("B_v", B_v, act), A("out", out, act, rows),
+           keep, num_pages, _factor(A, "B_k", B_k, cfg, rk), _factor(A, "B_v", B_v, cfg, rv), A("out", out, act, rows),
            A("lse", lse, _F32, rows[:3]), A("workspace", workspace, None),
            workspace.numel() * workspace.element_size(), num_splits, stream=stream)
 

@@ -27,11 +27,16 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunk = 128;   // pages one CTA scores
 constexpr int kVec = 8;          // channels per lane and pass
+constexpr int kHeads = 2;        // passes (groups of 32 / (d_h / kVec) heads) taken per page visit
+constexpr int kAhead = 2;        // pages a warp has in flight
+static_assert(kHeads == 2 && kAhead == 2, "the sums of a visit are folded by two");
+constexpr int kKeys = 4096;      // scores of a list kept in shared memory while it is cut
 
 struct SelectArgs {
   int batch, Q, H, G, gs, d_h, W, P;
   int max_pages, num_pages, n_first, n_last, K, chunk, chunks;
   int rope, causal;
+  int key_room;          // keys the dynamic shared memory holds
   const void* q;
   const int32_t* q_pos;
   const void* bounds;
@@ -66,22 +71,59 @@ __device__ __forceinline__ unsigned long long key_of(double v) {
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
 
+// The lo and hi entries of one lane's channels.  The larger of q·lo and q·hi is the
+// product with hi where q >= 0, else with lo: a bit select under masks that follow
+// the signs of q, so one entry per channel is unpacked and converted.
 template <int DT>
-__device__ __forceinline__ void load_vec(const typename Dt<DT>::T* p, float* v) {
+struct Box {
   using T = typename Dt<DT>::T;
-  constexpr int kWords = kVec * sizeof(T) / 16;
-  uint4 raw[kWords];
+  static constexpr int kWords = kVec * sizeof(T) / 4;      // 32-bit words per side
+  uint4 lo[kWords / 4], hi[kWords / 4];
+  __device__ __forceinline__ void load(const T* p, int W) {
 #pragma unroll
-  for (int w = 0; w < kWords; ++w) raw[w] = __ldg(reinterpret_cast<const uint4*>(p) + w);
-  const T* e = reinterpret_cast<const T*>(raw);
+    for (int w = 0; w < kWords / 4; ++w) {
+      lo[w] = __ldg(reinterpret_cast<const uint4*>(p) + w);
+      hi[w] = __ldg(reinterpret_cast<const uint4*>(p + W) + w);
+    }
+  }
+  __device__ __forceinline__ static void masks(const double* q, uint32_t* m) {
+    T ones[kVec];
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) v[k] = Dt<DT>::to_f(e[k]);
+    for (int k = 0; k < kVec; ++k) {
+      if constexpr (sizeof(T) == 4) ones[k] = __uint_as_float(q[k] >= 0.0 ? 0xffffffffu : 0u);
+      else {
+        const uint16_t b = q[k] >= 0.0 ? 0xffffu : 0u;
+        ones[k] = *reinterpret_cast<const T*>(&b);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) m[w] = reinterpret_cast<const uint32_t*>(ones)[w];
+  }
+  __device__ __forceinline__ double dot(const double* q, const uint32_t* m) const {
+    uint32_t e[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+      e[w] = (reinterpret_cast<const uint32_t*>(hi)[w] & m[w]) | (reinterpret_cast<const uint32_t*>(lo)[w] & ~m[w]);
+    const T* v = reinterpret_cast<const T*>(e);
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) s = fma(q[k], (double)Dt<DT>::to_f(v[k]), s);
+    return s;
+  }
+};
+
+// x of the lanes whose `bit` is clear and y of the others, each summed over the
+// lane pair that differs in that bit.
+__device__ __forceinline__ double fold(double x, double y, int bit, int lane) {
+  const bool up = lane & bit;
+  const double mine = up ? y : x, other = up ? x : y;
+  return mine + __shfl_xor_sync(0xffffffffu, other, bit);
 }
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_constant__ SelectArgs a) {
   using T = typename Dt<DT>::T;
-  extern __shared__ double qr[];               // [gs][d_h] rotated query
+  extern __shared__ double qr[];               // [gs][d_h] rotated query, [d_h] cosines and sines; later the keys
   __shared__ double best[kMaxChunk];           // this CTA's page scores
   __shared__ int pages[kMaxChunk];             // physical pages (-1: outside the pool)
   __shared__ int is_last;
@@ -111,41 +153,67 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     __syncthreads();   // the previous query is done with qr and best
     const int qpos = a.q_pos[(size_t)b * a.Q + j];
     const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Q + j) * a.H + (size_t)g * a.gs) * a.d_h;
+    double* cs = qr + a.gs * a.d_h;
+    for (int f = tid; f < half; f += kThreads) {   // one angle serves every head
+      double c = 1.0, s = 0.0;
+      if (a.rope) rope_cs_double(qpos, a.omega[f], c, s);
+      cs[f] = c;
+      cs[half + f] = s;
+    }
+    __syncthreads();
     for (int i = tid; i < a.gs * half; i += kThreads) {
       const int h = i / half, f = i - h * half;
       const double x1 = (double)Dt<DT>::to_f(q[h * a.d_h + f]), x2 = (double)Dt<DT>::to_f(q[h * a.d_h + half + f]);
-      double c = 1.0, s = 0.0;
-      if (a.rope) rope_cs_double(qpos, a.omega[f], c, s);
+      const double c = cs[f], s = cs[half + f];
       qr[h * a.d_h + f] = x1 * c - x2 * s;
       qr[h * a.d_h + half + f] = x2 * c + x1 * s;
     }
     __syncthreads();
     const int n = p1 - p0;
     if constexpr (VEC) {
-      // lanes_h lanes per head, heads_w heads per pass
+      // lanes_h lanes per head (4, 8 or 16), heads_w heads per pass
       const int lanes_h = a.d_h / kVec, heads_w = 32 / lanes_h;
       const int hl = lane / lanes_h, c0 = (lane % lanes_h) * kVec;
-      for (int h0 = 0; h0 < a.gs; h0 += heads_w) {
-        const int h = h0 + hl;
-        const bool on = h < a.gs;
-        double qv[kVec];
+      for (int h0 = 0; h0 < a.gs; h0 += kHeads * heads_w) {
+        double qv[kHeads][kVec];
+        uint32_t mask[kHeads][Box<DT>::kWords];
+        bool on[kHeads];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) qv[k] = on ? qr[h * a.d_h + c0 + k] : 0.0;
-        for (int i = warp; i < n; i += kWarps) {
-          const int pg = pages[i];
-          double s = 0.0;
-          if (on && pg >= 0) {
-            const T* lo = bounds + ((size_t)pg * a.G + g) * 2 * a.W + h * a.d_h + c0;
-            float vl[kVec], vh[kVec];
-            load_vec<DT>(lo, vl);
-            load_vec<DT>(lo + a.W, vh);
+        for (int u = 0; u < kHeads; ++u) {
+          const int h = h0 + u * heads_w + hl;
+          on[u] = h < a.gs;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) s = fma(qv[k], (double)(qv[k] >= 0.0 ? vh[k] : vl[k]), s);
+          for (int k = 0; k < kVec; ++k) qv[u][k] = on[u] ? qr[h * a.d_h + c0 + k] : 0.0;
+          Box<DT>::masks(qv[u], mask[u]);
+        }
+        const T* mine = bounds + (size_t)g * 2 * a.W + (h0 + hl) * a.d_h + c0;
+        // two pages side by side: their loads are all in flight before the first sum
+        for (int i0 = warp * kAhead; i0 < n; i0 += kWarps * kAhead) {
+          Box<DT> box[kAhead][kHeads];
+          bool live[kAhead];
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            const int pg = i0 + y < n ? pages[i0 + y] : -1;
+            live[y] = pg >= 0;
+#pragma unroll
+            for (int u = 0; u < kHeads; ++u)
+              if (live[y] && on[u]) box[y][u].load(mine + (size_t)pg * a.G * 2 * a.W + u * heads_w * a.d_h, a.W);
           }
-          for (int off = 1; off < lanes_h; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-          if (!on || pg < 0 || s != s) s = -INFINITY;
-          for (int off = lanes_h; off < 32; off <<= 1) s = fmax(s, __shfl_xor_sync(0xffffffffu, s, off));
-          if (lane == 0) best[i] = h0 == 0 ? s : fmax(best[i], s);
+          // the four sums (two pages, two heads) of the lanes of a head: two folds leave the sum of
+          // page (lane / 2) % 2 and head lane % 2 spread over every fourth lane
+          double s[kAhead];
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y)
+            s[y] = fold(live[y] && on[0] ? box[y][0].dot(qv[0], mask[0]) : 0.0,
+                        live[y] && on[1] ? box[y][1].dot(qv[1], mask[1]) : 0.0, 1, lane);
+          double v = fold(s[0], s[1], 2, lane);
+          for (int off = 4; off < lanes_h; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+          const bool is_on = (lane & 1) ? on[1] : on[0], is_live = (lane & 2) ? live[1] : live[0];
+          if (!is_on || !is_live || v != v) v = -INFINITY;
+          v = fmax(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          for (int off = lanes_h; off < 32; off <<= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, off));
+          const int i = i0 + (lane >> 1);
+          if ((lane == 0 || lane == 2) && i < n) best[i] = h0 == 0 ? v : fmax(best[i], v);
         }
       }
     } else {
@@ -195,6 +263,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     const int m = min(a.K, seen);
     int need = m - (first + seen - tail);      // pages to keep among [first, tail)
     const double* sc = out + (size_t)j * a.max_pages;
+    unsigned long long* keys = reinterpret_cast<unsigned long long*>(qr);
+    const bool in_smem = seen <= a.key_room;
+    auto key = [&](int i) { return in_smem ? keys[i] : key_of(__ldcg(sc + i)); };
     const size_t li = ((size_t)b * a.Q + j) * a.G + g;
 
     // threshold: pages with a key above thr are kept, and the lowest `ties` of those equal to it
@@ -206,6 +277,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       unsigned long long lo = ~0ull, hi = 0;
       for (int i = first + tid; i < tail; i += kThreads) {
         const unsigned long long k = key_of(__ldcg(sc + i));
+        if (in_smem) keys[i] = k;
         lo = min(lo, k);
         hi = max(hi, k);
       }
@@ -232,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         hist[tid] = 0;
         __syncthreads();
         for (int i = first + tid; i < tail; i += kThreads) {
-          const unsigned long long d = key_of(__ldcg(sc + i)) - base;
+          const unsigned long long d = key(i) - base;
           if (bits >= 64 || (d >> bits) == 0) atomicAdd(&hist[(d >> shift) & 255], 1u);
         }
         __syncthreads();
@@ -277,10 +349,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     for (int i0 = 0; i0 < seen; i0 += kThreads) {
       const int i = i0 + tid;
       const bool in = i < seen;
-      const double v = in ? __ldcg(sc + i) : 0.0;
       bool keep = in && (i < first || i >= tail);
-      const unsigned long long k = key_of(v);
       const bool mid = in && !keep;
+      const unsigned long long k = mid && thr != ~0ull && thr != 0 ? key(i) : 1;
       if (mid && k > thr) keep = true;
       const bool tie = mid && ties > 0 && k == thr;
       const unsigned below = (1u << lane) - 1;
@@ -307,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       }
       if (keep && at < a.K) {
         list[at] = i;
-        if (so != nullptr) so[at] = (float)v;
+        if (so != nullptr) so[at] = (float)__ldcg(sc + i);
       }
       done += all;
       __syncthreads();
@@ -323,19 +394,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Pages per CTA: about 4 CTAs for each SM, from one page per warp up.
+// Pages per CTA: about 6 CTAs for each of the 148 SMs, from one visit of every warp up.
 int chunk_of(long long lists, int max_pages) {
-  const long long ctas = 4 * 148;
+  const long long ctas = 6 * 148;
   long long c = ((long long)max_pages * lists + ctas - 1) / ctas;
-  c = (c + kWarps - 1) / kWarps * kWarps;
-  return (int)(c < kWarps ? kWarps : c > kMaxChunk ? kMaxChunk : c);
+  const int visit = kWarps * kAhead;
+  c = (c + visit - 1) / visit * visit;
+  return (int)(c < visit ? visit : c > kMaxChunk ? kMaxChunk : c);
 }
 
 template <int DT>
-cudaError_t launch(const SelectArgs& a, cudaStream_t st) {
+cudaError_t launch(SelectArgs a, cudaStream_t st) {
   const dim3 grid(a.chunks, a.G, a.batch);
-  const size_t smem = sizeof(double) * a.gs * a.d_h;
-  const bool vec = a.d_h % kVec == 0 && (a.d_h / kVec & (a.d_h / kVec - 1)) == 0 && a.d_h / kVec <= 32;
+  a.key_room = a.max_pages < kKeys ? a.max_pages : kKeys;
+  const int room = a.gs * a.d_h + a.d_h > a.key_room ? a.gs * a.d_h + a.d_h : a.key_room;
+  const size_t smem = sizeof(double) * room;
+  const int lanes_h = a.d_h / kVec;   // lanes a head takes in the vector form
+  const bool vec = a.d_h % kVec == 0 && (lanes_h == 4 || lanes_h == 8 || lanes_h == 16);
   auto kern = vec ? select_kernel<DT, true> : select_kernel<DT, false>;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

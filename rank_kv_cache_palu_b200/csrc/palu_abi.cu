@@ -57,18 +57,31 @@ palu_status check_config(const palu_config* c) {
   return PALU_OK;
 }
 
+// RoPE frequencies of a config as 64-bit fixed-point turns.  The 64 long-double
+// powers cost ~16 us, more than a small step's launches, so each thread keeps the
+// table of the last (base, head_dim) it computed.
 void fill_omega(const palu_config* c, uint64_t* omega) {
-  const int half = c->head_dim / 2;
-  const long double two_pi = 6.283185307179586476925286766559005768L;
-  for (int i = 0; i < palu::kMaxHalfDim; ++i) {
-    if (i >= half || c->rope_base == 0.f) {
-      omega[i] = 0;
-      continue;
+  static thread_local struct {
+    float base = -1.f;
+    int d = 0;
+    uint64_t omega[palu::kMaxHalfDim];
+  } kept;
+  if (kept.base != c->rope_base || kept.d != c->head_dim) {
+    const int half = c->head_dim / 2;
+    const long double two_pi = 6.283185307179586476925286766559005768L;
+    for (int i = 0; i < palu::kMaxHalfDim; ++i) {
+      if (i >= half || c->rope_base == 0.f) {
+        kept.omega[i] = 0;
+        continue;
+      }
+      const long double theta = powl((long double)c->rope_base, -2.0L * i / c->head_dim);
+      const long double turns = theta / two_pi;  // < 1
+      kept.omega[i] = (uint64_t)llroundl(ldexpl(turns, 64));  // 64-bit fixed-point fraction (< 2^62)
     }
-    const long double theta = powl((long double)c->rope_base, -2.0L * i / c->head_dim);
-    const long double turns = theta / two_pi;  // < 1
-    omega[i] = (uint64_t)llroundl(ldexpl(turns, 64));  // 64-bit fixed-point fraction (< 2^62)
+    kept.base = c->rope_base;
+    kept.d = c->head_dim;
   }
+  memcpy(omega, kept.omega, sizeof(kept.omega));
 }
 
 constexpr size_t kStatusBytes = sizeof(palu::DevStatus);

@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowsPerThread = 4;   // grid size: rows a thread is given before another CTA is started
+constexpr int kRowsPerThread = 4;   // rows a thread looks up side by side
 
 struct PlanArgs {
   int batch, P, max_pages, num_pages, n_rows;
@@ -63,7 +63,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 
 __device__ __forceinline__ int pages_of(long long tokens, int P) { return (int)((tokens + P - 1) / P); }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
   extern __shared__ int32_t smem[];
   int32_t* start = smem;                  // [batch + 1] first row of each sequence
   int32_t* len = start + a.batch + 1;     // [batch] length before the call
@@ -123,31 +123,46 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   }
   __syncthreads();
 
-  // this CTA's rows
+  // this CTA's rows: kRowsPerThread lookups side by side, so their loads overlap
   const int total_rows = start[a.batch];
-  for (long long r = (long long)blockIdx.x * kThreads + tid; r < a.n_rows; r += (long long)gridDim.x * kThreads) {
-    int slot = -1, pos = 0;
-    if (r < total_rows) {
+  for (long long r0 = (long long)blockIdx.x * kThreads * kRowsPerThread + tid; r0 < a.n_rows;
+       r0 += (long long)gridDim.x * kThreads * kRowsPerThread) {
+    int b[kRowsPerThread], pos[kRowsPerThread], off[kRowsPerThread], page[kRowsPerThread];
+#pragma unroll
+    for (int k = 0; k < kRowsPerThread; ++k) {
+      const long long r = r0 + k * kThreads;
+      b[k] = -1;
+      pos[k] = off[k] = page[k] = 0;
+      if (r >= total_rows) continue;
       int lo = 0, hi = a.batch - 1;         // the last sequence whose first row is <= r
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (start[mid] <= r) lo = mid;
         else hi = mid - 1;
       }
-      const int b = lo;
-      if (take[b] > 0) {
-        pos = len[b] + (int)(r - start[b]);
-        const int lp = pos / a.P, off = pos - lp * a.P;
-        const int fresh = lp - pages_of(len[b], a.P);   // >= 0: a page taken by this call
-        int32_t* entry = a.page_table + (size_t)b * a.max_pages + lp;
-        const int page = fresh >= 0 ? a.free_pages[F - 1 - before[b] - fresh] : *entry;
-        if (fresh >= 0 && off == 0) *entry = page;      // every new page starts with a new token
-        if (page < 0 || page >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b);
-        else slot = page * a.P + off;
-      }
+      if (take[lo] <= 0) continue;
+      b[k] = lo;
+      pos[k] = len[lo] + (int)(r - start[lo]);
+      const int lp = pos[k] / a.P;
+      off[k] = pos[k] - lp * a.P;
+      const int fresh = lp - pages_of(len[lo], a.P);   // >= 0: a page taken by this call
+      page[k] = fresh >= 0 ? a.free_pages[F - 1 - before[lo] - fresh] : a.page_table[(size_t)lo * a.max_pages + lp];
     }
-    a.slots[r] = slot;
-    a.positions[r] = pos;
+#pragma unroll
+    for (int k = 0; k < kRowsPerThread; ++k) {
+      const long long r = r0 + k * kThreads;
+      if (r >= a.n_rows) continue;
+      int slot = -1;
+      if (b[k] >= 0) {
+        const int lp = pos[k] / a.P;
+        if (off[k] == 0 && lp >= pages_of(len[b[k]], a.P))   // every new page starts with a new token
+          a.page_table[(size_t)b[k] * a.max_pages + lp] = page[k];
+        if (page[k] < 0 || page[k] >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b[k]);
+        else slot = page[k] * a.P + off[k];
+      }
+      a.slots[r] = slot;
+      a.positions[r] = pos[k];
+    }
   }
 
   // the last CTA to get here updates what every CTA has read
@@ -187,27 +202,35 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
   __syncthreads();
   const long long left = F - taken_pages;     // stack height before the pages given back
   if (given > 0) {
-    // page j (in (sequence, page) order) of those given back goes to left + given - 1 - j
+    // page j (in (sequence, page) order) of those given back goes to left + given - 1 - j;
+    // `start` now holds each sequence's first such page, so that every page has a thread
     long long done = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
       const int b = b0 + tid;
-      int has = 0, had = 0;
-      if (b < a.batch && take[b] < 0) {
-        had = pages_of(len[b], a.P);
-        has = pages_of((long long)len[b] + take[b], a.P);
-      }
+      int pages = 0;
+      if (b < a.batch && take[b] < 0)
+        pages = pages_of(len[b], a.P) - pages_of((long long)len[b] + take[b], a.P);
       long long total;
-      const long long j0 = done + block_scan(had - has, warp_sums, total);
+      const long long j0 = done + block_scan(pages, warp_sums, total);
       done += total;
-      for (int lp = has; lp < had; ++lp) {
-        int32_t* entry = a.page_table + (size_t)b * a.max_pages + lp;
-        const long long at = left + given - 1 - (j0 + lp - has);
-        const int page = *entry;
-        if (page < 0 || page >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b);
-        if (at < a.num_pages) a.free_pages[at] = page;
-        else report(a.st, PALU_ERR_DEVICE_BOUNDS, 4000001);   // more pages given back than the pool has
-        *entry = -1;
+      if (b < a.batch) start[b] = (int)min(j0, (long long)INT32_MAX);
+    }
+    __syncthreads();
+    for (long long j = tid; j < given; j += kThreads) {
+      int lo = 0, hi = a.batch - 1;         // the last sequence whose first page is <= j
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= j) lo = mid;
+        else hi = mid - 1;
       }
+      const int lp = pages_of((long long)len[lo] + take[lo], a.P) + (int)(j - start[lo]);
+      int32_t* entry = a.page_table + (size_t)lo * a.max_pages + lp;
+      const int page = *entry;
+      *entry = -1;
+      if (page < 0 || page >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + lo);
+      const long long at = left + given - 1 - j;
+      if (at < a.num_pages) a.free_pages[at] = page;
+      else report(a.st, PALU_ERR_DEVICE_BOUNDS, 4000001);   // more pages given back than the pool has
     }
   }
   for (int b = tid; b < a.batch; b += kThreads)
@@ -257,7 +280,7 @@ extern "C" palu_status palu_plan_append(int page_size, int batch, int max_pages,
   }
   const long long per = (long long)palu::kThreads * palu::kRowsPerThread;
   long long grid = ((long long)n_rows + per - 1) / per;
-  grid = grid < 1 ? 1 : grid > 2 * 148 ? 2 * 148 : grid;
+  grid = grid < 1 ? 1 : grid > 8 * 148 ? 8 * 148 : grid;
   palu::plan_kernel<<<(int)grid, palu::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   palu::count_launch();
   return palu::cuda_status(cudaGetLastError());

@@ -12,11 +12,10 @@
 // 32-bit numbers is exact there, and two orders of summation differ by ~1e-16 of
 // the total, far below one weight.
 //
-// A row is cut into chunks, one CTA each; each CTA leaves its chunk's sum in the
-// workspace, and the sequence's last CTA (a ticket) adds the sums in order, finds
-// the chunk where the running sum crosses u·total and looks through that chunk
-// alone.  Every order of addition is fixed, so results do not change from call to
-// call.
+// A row is cut into groups of 256 entries; every warp leaves the sums of its groups
+// in the workspace, and the sequence's last CTA (a ticket) finds the group where the
+// running sum crosses u·total and one warp looks through that group alone.  Every
+// order of addition is fixed, so results do not change from call to call.
 #include "palu_common.cuh"
 #include "palu_internal.h"
 
@@ -25,10 +24,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMinChunk = 2048;
+constexpr int kGroup = 256;   // entries one partial sum covers: a warp's, 8 a lane
+constexpr int kAhead = 2;     // groups a warp has in flight
 
 struct VerifyArgs {
-  int D, V, chunk, chunks;
+  int D, V, share, groups;
   const void* target;
   const void* draft;
   long long target_ld, draft_ld;
@@ -41,17 +41,16 @@ struct VerifyArgs {
   int32_t* rollback;
   DevStatus* st;
   unsigned* tickets;   // [batch]
-  double* sums;        // [batch][chunks]
+  double* sums;        // [batch][groups]
 };
 
-// Entries per chunk: enough CTAs to fill the GPU (about 8 of 148 each) for any
-// batch, but no chunk below kMinChunk entries, where the CTAs would cost more
-// than the reads they spread.
-int chunk_of(int batch, int vocab) {
-  const long long ctas = 148 * 8;
-  long long c = ((long long)vocab * (batch > 0 ? batch : 1) + ctas - 1) / ctas;
-  c = (c + kThreads - 1) / kThreads * kThreads;
-  return (int)(c < kMinChunk ? kMinChunk : c);
+// Groups per CTA: about four CTAs for each of the 148 SMs whatever the batch, but at
+// least one group for every warp, below which CTAs cost more than the reads they spread.
+int share_of(int batch, int groups) {
+  const long long ctas = 148 * 4;
+  long long c = ((long long)groups * (batch > 0 ? batch : 1) + ctas - 1) / ctas;
+  c = (c + kWarps - 1) / kWarps * kWarps;
+  return (int)(c < kWarps ? kWarps : c);
 }
 
 // Sum over the block, the same on every thread and in every run.
@@ -67,91 +66,190 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
   return s;
 }
 
-template <int DT>
+// The row of weights a token is drawn from.  VEC: rows start on 16 bytes and are
+// read 8 entries at a time; else entry by entry, coalesced across the warp.
+template <int DT, bool VEC>
 struct Row {
   using T = typename Dt<DT>::T;
+  static constexpr int kWords = 8 * sizeof(T) / 16;   // 16-byte words per 8 entries
   const T* p;
   const T* q;     // NULL: nothing is subtracted, but for the certain draft x
   int x;          // token of a refused draft that was certain, else -1
-  __device__ __forceinline__ double weight(int v) const {
-    const double a = (double)Dt<DT>::to_f(p[v]);
-    const double b = q != nullptr ? (double)Dt<DT>::to_f(q[v]) : v == x ? 1.0 : 0.0;
-    const double w = a - b;
+
+  __device__ __forceinline__ static double weight_of(float a, float b) {
+    const double w = (double)a - (double)b;
     return w > 0.0 && w < (double)INFINITY ? w : 0.0;
   }
-  // Σ weights of [v0, v1), this thread's share: every kThreads-th entry
-  __device__ __forceinline__ double share(int v0, int v1) const {
+  __device__ __forceinline__ double weight(int v) const {
+    return weight_of(Dt<DT>::to_f(p[v]), q != nullptr ? Dt<DT>::to_f(q[v]) : v == x ? 1.f : 0.f);
+  }
+  // Σ of 8 weights, exactly as in float64.  The difference of two 16-bit numbers is
+  // nearly always a float32 (a - (a - b) gives b back exactly when it is): then one
+  // conversion an entry does; a group with any other entry is summed anew.
+  __device__ __forceinline__ static double sum_of(const float* a, const float* b) {
     double s = 0.0;
-    int v = v0 + (int)threadIdx.x;
-    if (q != nullptr) {
-      for (; v + 7 * kThreads < v1; v += 8 * kThreads) {
-        T a[8], b[8];
+    if constexpr (DT != PALU_F32) {
+      bool fine = true;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          a[k] = p[v + k * kThreads];
-          b[k] = q[v + k * kThreads];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const double w = (double)Dt<DT>::to_f(a[k]) - (double)Dt<DT>::to_f(b[k]);
-          s += w > 0.0 && w < (double)INFINITY ? w : 0.0;
-        }
+      for (int k = 0; k < 8; ++k) {
+        const float d = a[k] - b[k];
+        fine = fine && a[k] - d == b[k] && d < INFINITY;
+        s += (double)fmaxf(d, 0.f);
       }
+      if (fine) return s;
+      s = 0.0;
     }
-    for (; v < v1; v += kThreads) s += weight(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += weight_of(a[k], b[k]);
     return s;
   }
-  // The first entry of [v0, v1) where base + the running sum exceeds `at` (-1: none does), and the
-  // last entry of positive weight (-1: none).  The whole block takes part and gets the answer.
-  __device__ int find(int v0, int v1, double base, double at, double* buf, int* ibuf) const {
-    const int per = (v1 - v0 + kThreads - 1) / kThreads;
-    const int a = min(v1, v0 + (int)threadIdx.x * per), b = min(v1, a + per);
-    double mine = 0.0;
-    int last = -1;
-    for (int v = a; v < b; ++v) {
-      const double w = weight(v);
-      mine += w;
-      if (w > 0.0) last = v;
-    }
-    // exclusive prefix over the threads
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    double s = mine;
+  // Σ weights of this lane's 8 entries of the group of 256 that starts at v0, which lies whole in the row
+  __device__ __forceinline__ double lane_sum(int v0) const {
+    const int lane = threadIdx.x & 31;
+    float a[8], b[8];
+    int at[8];
+    if constexpr (VEC) {
+      uint4 ra[kWords], rb[kWords];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double o = __shfl_up_sync(0xffffffffu, s, off);
-      if (lane >= off) s += o;
-    }
-    if (lane == 31) buf[warp] = s;
-    if (threadIdx.x == 0) {
-      ibuf[0] = INT32_MAX;
-      ibuf[1] = -1;
-    }
-    __syncthreads();
-    double run = base + (s - mine);
-    for (int w = 0; w < warp; ++w) run += buf[w];
-    for (int v = a; v < b; ++v) {
-      const double w = weight(v);
-      run += w;
-      if (w > 0.0 && run > at) {
-        atomicMin(&ibuf[0], v);
-        break;
+      for (int w = 0; w < kWords; ++w) {
+        ra[w] = __ldg(reinterpret_cast<const uint4*>(p + v0 + 8 * lane) + w);
+        rb[w] = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q + v0 + 8 * lane) + w) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a[k] = Dt<DT>::to_f(reinterpret_cast<const T*>(ra)[k]);
+        b[k] = Dt<DT>::to_f(reinterpret_cast<const T*>(rb)[k]);
+        at[k] = v0 + 8 * lane + k;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        at[k] = v0 + 32 * k + lane;
+        a[k] = Dt<DT>::to_f(p[at[k]]);
+        b[k] = q != nullptr ? Dt<DT>::to_f(q[at[k]]) : 0.f;
       }
     }
-    if (last >= 0) atomicMax(&ibuf[1], last);
-    __syncthreads();
-    const int hit = ibuf[0] != INT32_MAX ? ibuf[0] : ibuf[1];
-    __syncthreads();
-    return hit;
+    if (x >= 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (at[k] == x) b[k] = 1.f;
+    }
+    return sum_of(a, b);
+  }
+  // Σ weights of the group of 256 entries that starts at v0 (the whole warp takes part and gets it)
+  __device__ __forceinline__ double group_sum(int v0, int V) const {
+    double s = 0.0;
+    if (v0 + kGroup <= V) {
+      s = lane_sum(v0);
+    } else {
+      const int v = v0 + 8 * ((int)threadIdx.x & 31);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (v + k < V) s += weight(v + k);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
+  }
+  // The first entry of the group at v0 where base + the running sum exceeds `at`; where rounding
+  // lets none do so the last entry of positive weight.  One warp; every lane gets the answer.
+  __device__ __forceinline__ int find(int v0, int V, double base, double at) const {
+    const int lane = threadIdx.x & 31, v = v0 + 8 * lane;
+    double w[8], s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      w[k] = v + k < V ? weight(v + k) : 0.0;
+      s += w[k];
+    }
+    double run = s;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const double o = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run += o;
+    }
+    run = base + (run - s);
+    int hit = INT32_MAX, last = -1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      run += w[k];
+      if (w[k] > 0.0) {
+        last = v + k;
+        if (run > at && hit == INT32_MAX) hit = v + k;
+      }
+    }
+    hit = __reduce_min_sync(0xffffffffu, hit);
+    last = __reduce_max_sync(0xffffffffu, last);
+    return hit != INT32_MAX ? hit : last;
   }
 };
 
-template <int DT>
+// Inclusive sum of s over the warp.
+__device__ __forceinline__ double warp_scan(double s) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double o = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += o;
+  }
+  return s;
+}
+
+// The draw, by one CTA, from the group sums of the whole row: the first group whose running sum
+// passes u·total (the last one of positive sum if rounding hides it), then the entry within it.
+// -1: no positive weight.
+template <class R>
+__device__ int draw(const R& row, const double* sums, int groups, int V, float u, double* buf, int* ibuf) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  double part = 0.0;
+  for (int i = tid; i < groups; i += kThreads) part += __ldcg(sums + i);
+  const double total = block_sum(part, buf);
+  if (!(total > 0.0)) return -1;
+  const double at = (double)u * total;
+  if (tid == 0) {
+    ibuf[0] = INT32_MAX;
+    ibuf[1] = -1;
+  }
+  double run = 0.0, base = 0.0;   // base: the running sum ahead of this thread's group
+  int won = -1;
+  for (int g0 = 0; g0 < groups; g0 += kThreads) {
+    const int i = g0 + tid;
+    const double s = i < groups ? __ldcg(sums + i) : 0.0;
+    const double upto = warp_scan(s);
+    if (lane == 31) buf[warp] = upto;
+    __syncthreads();
+    double ahead = run;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) ahead += buf[w];
+      run += buf[w];
+    }
+    if (s > 0.0) {
+      base = ahead + (upto - s);
+      won = i;
+      if (ahead + upto > at) atomicMin(&ibuf[0], i);
+      atomicMax(&ibuf[1], i);
+    }
+    __syncthreads();
+    if (ibuf[0] != INT32_MAX) break;
+  }
+  const int group = ibuf[0] != INT32_MAX ? ibuf[0] : ibuf[1];
+  if (won == group) buf[0] = base;
+  __syncthreads();
+  if (warp == 0) {
+    const int hit = row.find(group * kGroup, V, buf[0], at);
+    if (lane == 0) ibuf[2] = hit;
+  }
+  __syncthreads();
+  return ibuf[2];
+}
+
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   using T = typename Dt<DT>::T;
   __shared__ double buf[kWarps];
-  __shared__ int ibuf[2];
+  __shared__ int ibuf[3];
   __shared__ int accepted, is_last;
-  const int b = blockIdx.y, tid = threadIdx.x;
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int n = a.draft_lens != nullptr ? a.draft_lens[b] : a.D;
   if (n < 0 || n > a.D) {
     if (blockIdx.x == 0 && tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 1000000 + b);
@@ -162,89 +260,93 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   const int32_t* xs = a.draft_tokens + (size_t)b * a.D;
   if (tid < 32) {   // one lane per draft (PALU_MAX_DRAFTS = 32)
     bool yes = false;
-    if (tid < n) {
-      const int x = xs[tid];
-      if (x < 0 || x >= a.V) {
-        if (blockIdx.x == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 2000000 + b);
-      } else {
+    if (tid < a.D) {
+      const int x = xs[tid];                                    // independent of n: its load overlaps n's
+      const float u = a.u_accept[(size_t)b * a.D + tid];
+      const bool in = x >= 0 && x < a.V;
+      if (!in && tid < n && blockIdx.x == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 2000000 + b);
+      if (in) {
         const double p = (double)Dt<DT>::to_f(target[(size_t)tid * a.target_ld + x]);
         const double q = draft != nullptr ? (double)Dt<DT>::to_f(draft[(size_t)tid * a.draft_ld + x]) : 1.0;
-        yes = (double)a.u_accept[(size_t)b * a.D + tid] * q < p;
+        yes = tid < n && (double)u * q < p;
       }
     }
     const unsigned no = ~__ballot_sync(0xffffffffu, yes);
-    if (tid == 0) accepted = no == 0 ? 32 : __ffs(no) - 1;   // n <= 32 lanes can say yes
+    if (tid == 0) accepted = no == 0 ? 32 : __ffs(no) - 1;      // n <= 32 lanes can say yes
   }
   __syncthreads();
   const int acc = accepted;
   const bool refused = acc < n;
-  Row<DT> row;
+  Row<DT, VEC> row;
   row.p = target + (size_t)acc * a.target_ld;
   row.q = refused && draft != nullptr ? draft + (size_t)acc * a.draft_ld : nullptr;
   row.x = refused && draft == nullptr ? xs[acc] : -1;
-  const int v0 = blockIdx.x * a.chunk, v1 = min(a.V, v0 + a.chunk);
-  const double mine = block_sum(row.share(v0, v1), buf);
-
-  if (a.chunks > 1) {
-    if (tid == 0) {
-      a.sums[(size_t)b * a.chunks + blockIdx.x] = mine;
-      __threadfence();
-      is_last = atomicAdd(&a.tickets[b], 1u) == (unsigned)a.chunks - 1;
+  double* sums = a.sums + (size_t)b * a.groups;
+  auto sum_groups = [&](int g0, int g1) {      // kAhead groups a warp side by side
+    for (int g = g0 + warp * kAhead; g < g1; g += kWarps * kAhead) {
+      double s[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s[k] = g + k < g1 ? row.group_sum((g + k) * kGroup, a.V) : 0.0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (lane == 0 && g + k < g1) sums[g + k] = s[k];
     }
+  };
+  sum_groups(blockIdx.x * a.share, min(a.groups, (int)(blockIdx.x + 1) * a.share));
+
+  if (gridDim.x > 1) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) is_last = atomicAdd(&a.tickets[b], 1u) == gridDim.x - 1;
     __syncthreads();
     if (!is_last) return;
     __threadfence();
+  } else {
+    __syncthreads();
   }
   // the sequence's last CTA draws the token
-  const double* sums = a.sums + (size_t)b * a.chunks;
-  double total = 0.0;
-  for (int c = 0; c < a.chunks; ++c) total += a.chunks > 1 ? __ldcg(sums + c) : mine;
-  int hit = -1;
-  if (total > 0.0) {
-    const double at = (double)a.u_sample[b] * total;
-    double base = 0.0;
-    int c = 0, live = 0;       // live: the last chunk of positive sum, where a running sum cut short ends
-    double live_base = 0.0;
-    for (; c < a.chunks; ++c) {
-      const double s = a.chunks > 1 ? __ldcg(sums + c) : mine;
-      if (s > 0.0) {
-        live = c;
-        live_base = base;
-        if (base + s > at) break;
-      }
-      base += s;
-    }
-    hit = row.find(live * a.chunk, min(a.V, (live + 1) * a.chunk), live_base, at, buf, ibuf);
-  } else if (refused) {
+  const float u = a.u_sample[b];
+  int hit = draw(row, sums, a.groups, a.V, u, buf, ibuf);
+  if (hit < 0 && refused) {
     // p <= q everywhere: the target's own row
     row.q = nullptr;
     row.x = -1;
-    total = block_sum(row.share(0, a.V), buf);
-    if (total > 0.0) hit = row.find(0, a.V, 0.0, (double)a.u_sample[b] * total, buf, ibuf);
+    sum_groups(0, a.groups);
+    __threadfence();
+    __syncthreads();
+    hit = draw(row, sums, a.groups, a.V, u, buf, ibuf);
   }
   for (int i = tid; i <= a.D; i += kThreads)
     a.tokens[(size_t)b * (a.D + 1) + i] = i < acc ? xs[i] : i == acc ? hit : -1;
   if (tid == 0) {
     a.num_accepted[b] = acc;
     if (a.rollback != nullptr) a.rollback[b] = acc - n;
-    if (a.chunks > 1) a.tickets[b] = 0;
+    if (gridDim.x > 1) a.tickets[b] = 0;
   }
+}
+
+template <int DT>
+void launch(const VerifyArgs& a, dim3 grid, cudaStream_t st) {
+  const long long elt = Dt<DT>::bytes;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) % 16 == 0 &&
+                   a.target_ld * elt % 16 == 0 && (a.draft == nullptr || a.draft_ld * elt % 16 == 0);
+  if (vec) verify_kernel<DT, true><<<grid, kThreads, 0, st>>>(a);
+  else verify_kernel<DT, false><<<grid, kThreads, 0, st>>>(a);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // The tickets follow the status word and have room for the largest batch, so that no call of other
-// sizes leaves anything but zeros there; then the chunk sums.
+// sizes leaves anything but zeros there; then the group sums.
 struct Layout {
-  int chunk, chunks;
+  int groups;
   size_t sums, total;
 };
 Layout layout(int batch, int vocab) {
   Layout l;
-  l.chunk = chunk_of(batch, vocab);
-  l.chunks = (vocab + l.chunk - 1) / l.chunk;
+  l.groups = (vocab + kGroup - 1) / kGroup;
   l.sums = sizeof(DevStatus) + sizeof(unsigned) * PALU_VERIFY_MAX_BATCH;
-  l.total = l.sums + align256(sizeof(double) * (size_t)batch * l.chunks);
+  l.total = l.sums + align256(sizeof(double) * (size_t)batch * l.groups);
   return l;
 }
 
@@ -289,17 +391,18 @@ extern "C" palu_status palu_verify_drafts(int dtype, int batch, int num_drafts, 
   for (const void* p : words)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return PALU_ERR_ALIGNMENT;
   char* ws = static_cast<char*>(workspace);
-  const palu::VerifyArgs a{num_drafts, vocab, l.chunk, l.chunks, target_probs,
+  const int share = palu::share_of(batch, l.groups);
+  const palu::VerifyArgs a{num_drafts, vocab, share, l.groups, target_probs,
                            num_drafts > 0 ? draft_probs : nullptr, target_ld, draft_ld, draft_tokens, draft_lens,
                            u_accept, u_sample, tokens, num_accepted, rollback,
                            reinterpret_cast<palu::DevStatus*>(ws),
                            reinterpret_cast<unsigned*>(ws + sizeof(palu::DevStatus)),
                            reinterpret_cast<double*>(ws + l.sums)};
-  const dim3 grid(l.chunks, batch);
+  const dim3 grid((l.groups + share - 1) / share, batch);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == PALU_F32) palu::verify_kernel<PALU_F32><<<grid, palu::kThreads, 0, st>>>(a);
-  else if (dtype == PALU_F16) palu::verify_kernel<PALU_F16><<<grid, palu::kThreads, 0, st>>>(a);
-  else palu::verify_kernel<PALU_BF16><<<grid, palu::kThreads, 0, st>>>(a);
+  if (dtype == PALU_F32) palu::launch<PALU_F32>(a, grid, st);
+  else if (dtype == PALU_F16) palu::launch<PALU_F16>(a, grid, st);
+  else palu::launch<PALU_BF16>(a, grid, st);
   palu::count_launch();
   return palu::cuda_status(cudaGetLastError());
 }
