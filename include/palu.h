@@ -413,10 +413,14 @@ palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int
  *   page_scores [batch][num_queries][G][list_len] float32 or NULL (written): the
  *              listed pages' scores, -inf behind them
  * A query sees every page of its sequence; with num_queries > 1 and no position
- * pool only those that hold a token at or before q_pos.  Scores are computed in
- * float64; of equal scores the lower page wins; a head's sum that is not a number
- * counts as -inf.  batch·G <= PALU_SELECT_MAX_LISTS (PALU_ERR_UNSUPPORTED above). */
+ * pool only those that hold a token at or before q_pos.  The choice is that of
+ * scores computed in float64 (page_scores are float32 sums, within 2^-20 Σ_c
+ * (|q_c| + |q_pair(c)|) |v_c| of them, v_c the bound taken); of equal scores
+ * the lower page wins; a head's sum that is not a number counts as -inf.
+ * batch·G <= PALU_SELECT_MAX_LISTS, max_pages <= PALU_SELECT_MAX_PAGES and
+ * group_size·head_dim <= 8192 (PALU_ERR_UNSUPPORTED above). */
 #define PALU_SELECT_MAX_LISTS 65536
+#define PALU_SELECT_MAX_PAGES 32768
 palu_status palu_select_workspace_size(const palu_config* cfg, int batch, int num_queries, int max_pages,
                                        size_t* bytes);
 palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries, const void* q,

@@ -745,13 +745,15 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
       num_last < 0 || list_len <= 0 || (long long)num_first + num_last > list_len)
     return PALU_ERR_INVALID_ARG;
   const long long G = cfg->num_heads / cfg->group_size;
-  if (batch * G > PALU_SELECT_MAX_LISTS || batch > 65535 || (long long)cfg->group_size * cfg->head_dim > 16384)
+  if (batch * G > PALU_SELECT_MAX_LISTS || batch > 65535 || max_pages > PALU_SELECT_MAX_PAGES ||
+      (long long)cfg->group_size * cfg->head_dim > 8192)
     return PALU_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < palu::select_workspace(cfg, batch, num_queries, max_pages))
     return PALU_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
   if (batch == 0) return PALU_OK;
-  if (!q || !q_pos || !bounds || !page_table || !seq_lens || !page_list || !page_counts) return PALU_ERR_INVALID_ARG;
+  if (!q || !q_pos || !bounds || !page_table || !seq_lens || !page_list || !page_counts || num_pages == 0)
+    return PALU_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(bounds)) return PALU_ERR_ALIGNMENT;
   uint64_t omega[palu::kMaxHalfDim];
   fill_omega(cfg, omega);

@@ -71,7 +71,6 @@ __device__ __forceinline__ double block_sum(double v, double* buf) {
 template <int DT, bool VEC>
 struct Row {
   using T = typename Dt<DT>::T;
-  static constexpr int kWords = 8 * sizeof(T) / 16;   // 16-byte words per 8 entries
   const T* p;
   const T* q;     // NULL: nothing is subtracted, but for the certain draft x
   int x;          // token of a refused draft that was certain, else -1
@@ -109,6 +108,7 @@ struct Row {
     float a[8], b[8];
     int at[8];
     if constexpr (VEC) {
+      constexpr int kWords = 8 * sizeof(T) / 16;
       uint4 ra[kWords], rb[kWords];
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
