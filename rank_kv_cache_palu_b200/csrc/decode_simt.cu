@@ -352,6 +352,7 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t st) {
+  if (a.segments != nullptr) return launch_pages_combine(a, st);
   const size_t smem = sizeof(float) * (a.r_v + a.S + 4 * a.d_h);
   dim3 grid(a.gm.n * a.gs, a.batch * a.qn);
   if (a.act == PALU_F32) combine_kernel<PALU_F32><<<grid, kCombineThreads, smem, st>>>(a);

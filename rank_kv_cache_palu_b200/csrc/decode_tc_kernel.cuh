@@ -41,7 +41,6 @@
 #include "palu_common.cuh"
 #include "palu_internal.h"
 #include "palu_tc.h"
-#include "sparse_list.cuh"
 #include "tc_ptx.cuh"
 
 namespace palu {
@@ -156,10 +155,7 @@ __device__ __forceinline__ int page_of(const DecodeArgs& a, int b, int lp) {
 
 // The producers read the table entry of a tile one tile before they use it
 // (raw, checked at the use), so the dependent load never stalls the copies.
-// Sparse: entry k of the CTA's list gives the logical page.
-template <bool SPARSE>
-__device__ __forceinline__ int page_ahead(const DecodeArgs& a, int b, const TileRange& tr, const ListRange& lr, int k) {
-  if constexpr (SPARSE) return k < lr.n ? list_page(a, lr, lr.list[k]) : -1;
+__device__ __forceinline__ int page_ahead(const DecodeArgs& a, int b, const TileRange& tr, int k) {
   return k < tr.ntiles ? a.page_table[(size_t)b * a.max_pages + tr.t_begin / kTile + k] : -1;
 }
 __device__ __forceinline__ bool page_valid(const DecodeArgs& a, int pg) { return pg >= 0 && pg < a.num_pages; }
@@ -271,11 +267,7 @@ __device__ __forceinline__ void trace_record(const DecodeArgs& a, int ev, int k,
 // CONTIG: token positions are the cache slots (no position pool).  A separate
 // instantiation keeps the per-token sincos path of explicit positions out of
 // the score loop's instruction footprint.
-// SPARSE: the CTA walks the pages of its query's list (palu_decode_attn_pages)
-// instead of a page range, in instantiations of their own (decode_pages.cu); P
-// then goes to the value MMA as hi + lo 16-bit numbers in rows h and h + 2 of its
-// 16 (the padding rows are paid for anyway), so no weight is rounded to 16 bits.
-template <int ACT, int NRV, int LAT, bool CONTIG, bool SPARSE = false>
+template <int ACT, int NRV, int LAT, bool CONTIG>
 __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_bk, const __grid_constant__ DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -302,10 +294,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
   const GroupMap& gm = a.gm;
   const int nkc = r_k / kChunk;
   const uint32_t k_blk_bytes = (uint32_t)a.P * (kInt4 ? r_k / 2 : 2 * r_k);   // this entry's block of a page
-  // the dense walk covers tiles of consecutive pages, the sparse one the pages of the list
-  ListRange lr{};
-  if constexpr (SPARSE) lr = list_range(a, b, gm.g[gi], st);
-  const TileRange tr = SPARSE ? TileRange{0, lr.T, lr.n, lr.ragged_last} : tile_range(a, b, st, threadIdx.x == 0);
+  const TileRange tr = tile_range(a, b, st, threadIdx.x == 0);
   const long long t_start = clock64();
   auto trace = [&](int ev, int k) {
     if (a.trace != nullptr) trace_record(a, ev, k, t_start);
@@ -430,11 +419,11 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       return true;
     };
     Slot s0, s1, s2, s3;                               // after the shift: chunks n, n+1, n+2; s3 takes n+3
-    for (int kk = 1; kk <= kPrefetch; ++kk) prefetch_page(page_ahead<SPARSE>(a, b, tr, lr, kk));
-    int pg_k = page_ahead<SPARSE>(a, b, tr, lr, 0);                // tile k of chunk n
-    int pg_k1 = page_ahead<SPARSE>(a, b, tr, lr, 1);               // tile k+1
-    int pg_k2 = page_ahead<SPARSE>(a, b, tr, lr, 2);               // tile k+2, in flight
-    int pf = page_ahead<SPARSE>(a, b, tr, lr, 1 + kPrefetch);      // tile k+1+kPrefetch, pulled into L2
+    for (int kk = 1; kk <= kPrefetch; ++kk) prefetch_page(page_ahead(a, b, tr, kk));
+    int pg_k = page_ahead(a, b, tr, 0);                // tile k of chunk n
+    int pg_k1 = page_ahead(a, b, tr, 1);               // tile k+1
+    int pg_k2 = page_ahead(a, b, tr, 2);               // tile k+2, in flight
+    int pf = page_ahead(a, b, tr, 1 + kPrefetch);      // tile k+1+kPrefetch, pulled into L2
     issue(0, s1, pg_k);
     issue(1, s2, pg_k);
     issue(2, s3, pg_k);
@@ -452,13 +441,13 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       if (c == 0 && n > 0) {
         pg_k = pg_k1;
         pg_k1 = pg_k2;
-        pg_k2 = page_ahead<SPARSE>(a, b, tr, lr, (n >> 2) + 2);
+        pg_k2 = page_ahead(a, b, tr, (n >> 2) + 2);
       }
       issue(n + 3, s3, c == 0 ? pg_k : pg_k1);
       if (!consume(n, s0)) break;
       if (c == 0) {
         prefetch_page(pf);
-        pf = page_ahead<SPARSE>(a, b, tr, lr, (n >> 2) + 2 + kPrefetch);
+        pf = page_ahead(a, b, tr, (n >> 2) + 2 + kPrefetch);
       }
     }
   } else if (warp >= 4) {
@@ -542,8 +531,8 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       o[32] = B;
       o[64] = -A;
     };
-    auto half_scores = [&](int slot, int tile, int pos, float* part, auto&& mid) {
-      const float* ab = abuf + (tile & 1) * 192;
+    auto half_scores = [&](int slot, int t0, int pos, float* part, auto&& mid) {
+      const float* ab = abuf + ((t0 / kTile) & 1) * 192;
       f2 acc[2][2];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) acc[hh][0] = acc[hh][1] = 0ull;
@@ -652,14 +641,8 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         const uint32_t sb = (uint32_t)((j + 1) & 1) * 256;
 #pragma unroll
         for (int mb = 0; mb < NRV; ++mb) {
-          float v = tmem_ld1(tmem + lane_addr + sb + mb * 32 + hw);
-          if constexpr (SPARSE) {
-            const float vl = tmem_ld1(tmem + lane_addr + sb + mb * 32 + hw + 2);   // the lo parts of P
-            tmem_wait_ld();
-            v += vl;
-          } else {
-            tmem_wait_ld();
-          }
+          const float v = tmem_ld1(tmem + lane_addr + sb + mb * 32 + hw);
+          tmem_wait_ld();
           acc[mb] = fmaf(acc[mb], scale, v);
         }
         return true;
@@ -668,25 +651,15 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       const int nv_tiles = tr.ntiles - (tr.ragged_last ? 1 : 0);   // tiles whose value sums are MMAs
       // causal bound (several queries per step): tokens after the query's position are masked
       const int qlim = a.causal ? a.q_pos[(size_t)b * a.qpos_bstride] : 0;
-      // logical page of tile k: sparse tiles are read one ahead of their use
-      int lp_next = SPARSE && tr.ntiles > 0 ? lr.list[0] : 0;
       if (contig && tr.ntiles > 0) {
-        if constexpr (SPARSE) post_rotated_query(lp_next * kTile, 0);
-        else post_rotated_query(tr.t_begin, (tr.t_begin / kTile) & 1);
+        post_rotated_query(tr.t_begin, (tr.t_begin / kTile) & 1);
         ok = ep_sync(37) && ok;
       }
       for (int k = 0; k < tr.ntiles && ok; ++k) {
-        const int t0 = SPARSE ? lp_next * kTile : tr.t_begin + k * kTile;
-        if (SPARSE && k + 1 < tr.ntiles) lp_next = lr.list[k + 1];
+        const int t0 = tr.t_begin + k * kTile;
         int pos = t0 + row;
         if (a.pos_pool != nullptr) {
-          int pg;
-          if constexpr (SPARSE) {
-            pg = list_page(a, lr, t0 / kTile);
-            if (!page_valid(a, pg)) pg = -1;
-          } else {
-            pg = page_of(a, b, t0 / kTile);
-          }
+          const int pg = page_of(a, b, t0 / kTile);
           pos = pg >= 0 ? a.pos_pool[(size_t)pg * a.P + row] : 0;
         }
         const bool valid = t0 + row < tr.t_end && (!a.causal || pos <= qlim);
@@ -697,14 +670,14 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         float part[2];
         // Halfway through the pass (score batches 0 and 1 read) the columns where the
         // previous tile's value MMA writes are dead: tell the MMA thread.
-        half_scores(slot, SPARSE ? k : t0 / kTile, pos, part, [&](int jj) {
+        half_scores(slot, t0, pos, part, [&](int jj) {
           if (jj != kNB / 2) return;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_MID));
         });
         // the next tile's rotated query; the tile-max sync below publishes it
-        if (contig) post_rotated_query(SPARSE ? lp_next * kTile : t0 + kTile, ((SPARSE ? k : t0 / kTile) + 1) & 1);
+        if (contig) post_rotated_query(t0 + kTile, ((t0 / kTile) + 1) & 1);
         psc[(slot * 2 + (1 - hw)) * 128 + row] = part[1 - hw];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_XCH + slot));
@@ -723,16 +696,9 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         const float m_new = fmaxf(m_run, mt);
         // 0 on the first tile; 1 while every token so far is masked
         const float scale = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);
-        const float pf = valid ? exp2f(sc - m_new) : 0.f;
-        const uint16_t pb = to_bits<ACT>(pf);
+        const uint16_t pb = to_bits<ACT>(valid ? exp2f(sc - m_new) : 0.f);
         *reinterpret_cast<uint16_t*>(sbase + L.p + slot * kPBytes + p_offset(hw, row)) = pb;
-        if constexpr (SPARSE) {
-          *reinterpret_cast<uint16_t*>(sbase + L.p + slot * kPBytes + p_offset(hw + 2, row)) =
-              to_bits<ACT>(pf - from_bits<ACT>(pb));
-          l_part = fmaf(l_part, scale, pf);
-        } else {
-          l_part = fmaf(l_part, scale, from_bits<ACT>(pb));
-        }
+        l_part = fmaf(l_part, scale, from_bits<ACT>(pb));
         m_run = m_new;
         fence_proxy_async();
         __syncwarp();
@@ -754,15 +720,9 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
           // partial last page: a += Σ_{valid tokens} p · z_v on CUDA cores,
           // reading only the valid rows (the rest of the page is never touched)
           ok = ep_sync(34);   // every P entry of this head is written
-          const int t0 = SPARSE ? lr.list[kl] * kTile : tr.t_begin + kl * kTile;
+          const int t0 = tr.t_begin + kl * kTile;
           const int nvalid = tr.t_end - t0;
-          int pg;
-          if constexpr (SPARSE) {
-            pg = list_page(a, lr, t0 / kTile);
-            if (!page_valid(a, pg)) pg = -1;
-          } else {
-            pg = page_of(a, b, t0 / kTile);
-          }
+          const int pg = page_of(a, b, t0 / kTile);
           float at[NRV];
 #pragma unroll
           for (int mb = 0; mb < NRV; ++mb) at[mb] = 0.f;
@@ -771,9 +731,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
             const uint8_t* zvs = kInt4 ? gm.zvs[gi] + (size_t)pg * gm.vs_page : nullptr;
             const uint8_t* pbuf = sbase + L.p + (kl & 1) * kPBytes;
             for (int t = 0; t < nvalid; ++t) {
-              float pv = from_bits<ACT>(*reinterpret_cast<const uint16_t*>(pbuf + p_offset(hw, t)));
-              if constexpr (SPARSE)
-                pv += from_bits<ACT>(*reinterpret_cast<const uint16_t*>(pbuf + p_offset(hw + 2, t)));
+              const float pv = from_bits<ACT>(*reinterpret_cast<const uint16_t*>(pbuf + p_offset(hw, t)));
               const uint8_t* srow = kInt4 ? zvs + (size_t)t * a.vs_row : nullptr;
 #pragma unroll
               for (int mb = 0; mb < NRV; ++mb)
@@ -866,9 +824,9 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         return true;
       };
       Slot s0, s1, s2;                                   // after the shift: stages n, n+1; s2 takes n+2
-      int pg_k = page_ahead<SPARSE>(a, b, tr, lr, 0);                // tile k of stage n
-      int pg_k1 = page_ahead<SPARSE>(a, b, tr, lr, 1);               // tile k+1
-      int pg_k2 = page_ahead<SPARSE>(a, b, tr, lr, 2);               // tile k+2, in flight
+      int pg_k = page_ahead(a, b, tr, 0);                // tile k of stage n
+      int pg_k1 = page_ahead(a, b, tr, 1);               // tile k+1
+      int pg_k2 = page_ahead(a, b, tr, 2);               // tile k+2, in flight
       issue(0, s1, pg_k);
       issue(1, s2, pg_k);
       // as for the keys: the slots shift before the next loads go out
@@ -879,7 +837,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         if (n % kSPT == 0 && n > 0) {
           pg_k = pg_k1;
           pg_k1 = pg_k2;
-          pg_k2 = page_ahead<SPARSE>(a, b, tr, lr, n / kSPT + 2);
+          pg_k2 = page_ahead(a, b, tr, n / kSPT + 2);
         }
         issue(n + 2, s2, (n + 2) / kSPT == n / kSPT ? pg_k : pg_k1);
         if (!consume(n, s0)) break;
@@ -892,11 +850,11 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         // No bulk L2 prefetch of later pages here: with the bulk copies of the two
         // head-pair CTAs of a group in flight, a prefetch 3 or 6 pages ahead left the
         // copy latency unchanged and the call 2-3 % slower.
-        int pg_next = page_ahead<SPARSE>(a, b, tr, lr, 0);
+        int pg_next = page_ahead(a, b, tr, 0);
         long long issued = 0;
         for (int k = 0; k < tr.ntiles && !*abort_flag; ++k) {
           int pg = pg_next;
-          pg_next = page_ahead<SPARSE>(a, b, tr, lr, k + 1);   // in flight during this tile's copies
+          pg_next = page_ahead(a, b, tr, k + 1);   // in flight during this tile's copies
           if (!page_valid(a, pg)) {
             report(st, PALU_ERR_DEVICE_BOUNDS, 2000000 + b);
             pg = 0;   // keep the pipeline fed from a valid page; the status says the result is void
@@ -919,12 +877,12 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       if (lane == 0) {
         int stage = 0;
         uint32_t phase = 0;
-        int pg_next = page_ahead<SPARSE>(a, b, tr, lr, 0);
+        int pg_next = page_ahead(a, b, tr, 0);
         long long issued = 0;
         for (int k = 0; k < tr.ntiles && !*abort_flag; ++k) {
           if (tr.ragged_last && k == tr.ntiles - 1) break;    // CUDA-core value sum for a partial page
           int pg = pg_next;
-          pg_next = page_ahead<SPARSE>(a, b, tr, lr, k + 1);   // in flight during this tile's copies
+          pg_next = page_ahead(a, b, tr, k + 1);   // in flight during this tile's copies
           if (!page_valid(a, pg)) pg = 0;   // reported by the z_k producer
           const uint8_t* src = gm.zv[gi] + (size_t)pg * gm.v_page;
           // one 16 KB copy per 128-byte column block of the page (64 latent entries of all
@@ -1160,7 +1118,7 @@ bool make_map_bk_paired(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt,
   return r == CUDA_SUCCESS;
 }
 
-template <int ACT, int NRV, int LAT, bool SPARSE = false>
+template <int ACT, int NRV, int LAT>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   const CUtensorMapDataType dt = ACT == PALU_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap tm_bk;
@@ -1177,8 +1135,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   }
   const Smem L = smem_layout(a.r_k, LAT == PALU_INT4);
   const size_t smem = L.total + 1024;
-  auto kern = a.pos_pool == nullptr ? decode_tc_kernel<ACT, NRV, LAT, true, SPARSE>
-                                    : decode_tc_kernel<ACT, NRV, LAT, false, SPARSE>;
+  auto kern = a.pos_pool == nullptr ? decode_tc_kernel<ACT, NRV, LAT, true> : decode_tc_kernel<ACT, NRV, LAT, false>;
   DecodeArgs args = a;
   const TraceSetting ts = trace_setting();
   const size_t ctas = (size_t)a.S * a.gm.n * (a.gs / 2) * a.batch;

@@ -322,6 +322,52 @@ size_t decode_workspace(const Layer& L, int batch, int Q, int max_pages, int num
   return kStatusBytes + part + fq;
 }
 
+// The walk of a sparse step's tensor-core launches (pages_walk.cuh): queries per
+// launch, CTAs per block column, and the workspace one launch and its combine use.
+struct WalkPlan {
+  int units, ctas;
+  size_t part, cont, segments, folded;   // bytes
+  size_t total() const { return part + cont + segments + folded; }
+};
+
+WalkPlan walk_plan(const palu_config* c, int kind, int batch, int Q, int list_len) {
+  const long long heads = c->num_heads, groups = heads / c->group_size;
+  const long long columns = kind == 3 ? groups : groups * palu::tc_head_blocks(c);
+  const long long max_tiles = 128LL * 148 * 8;     // of one column in one launch
+  WalkPlan p{};
+  long long seqs = 2048 / Q;                       // sequences a launch enumerates, whole ones
+  if (seqs * Q * list_len > max_tiles) seqs = max_tiles / ((long long)Q * list_len);
+  if (seqs < 1) seqs = 1;
+  if (seqs > batch) seqs = batch > 0 ? batch : 1;
+  p.units = (int)(seqs * Q);
+  const long long tiles = (long long)p.units * list_len;
+  long long ctas = 148 / columns;                  // one CTA per SM ...
+  if (ctas < (tiles + 127) / 128) ctas = (tiles + 127) / 128;   // ... and at most 128 tiles a CTA
+  if (ctas > tiles) ctas = tiles;
+  if (ctas < 1) ctas = 1;
+  p.ctas = (int)ctas;
+  const size_t stride = sizeof(float) * (c->rank_v + palu::kPartHead);
+  p.part = align256((size_t)p.units * heads * stride);
+  p.cont = align256((size_t)p.ctas * heads * stride);
+  p.segments = align256((size_t)p.units * groups * sizeof(int2));
+  p.folded = kind == 3 ? align256(palu::fused_query_bytes(c, p.units)) : 0;
+  return p;
+}
+
+size_t pages_workspace(const Layer& L, int batch, int Q, int list_len, int num_splits) {
+  size_t most = 0;
+  for (int c = 0; c < L.nset; ++c) {
+    const palu_config cc = set_cfg(L, c);
+    const int kind = kernel_kind(&cc);
+    const size_t n =
+        kind == 1 ? align256((size_t)batch * Q * cc.num_heads *
+                             run_S(&cc, kind, batch * Q, list_len, num_splits) * (cc.rank_v + 2) * sizeof(float))
+                  : walk_plan(&cc, kind, batch, Q, list_len).total();
+    if (n > most) most = n;
+  }
+  return kStatusBytes + most;
+}
+
 // The compress kernels take every group of the layer in one launch (output
 // columns follow the groups' ranks); the tensor-core kernel serves the layer
 // when it serves each group's rank pair.
@@ -406,8 +452,38 @@ palu_status compress_layer(const Layer& L, int n_tokens, int d_model, const void
 struct PageLists {
   const int32_t* list = nullptr;
   const int32_t* counts = nullptr;
-  int len = 0;
+  int len = 0, queries = 1;
 };
+
+// One decode set of a sparse step on the tensor-core kernels, a launch and its combine
+// per run of sequences.  `all` holds every query as a sequence of its own.
+cudaError_t walk_set(const palu::DecodeArgs& all, const WalkPlan& p, int kind, cudaStream_t st) {
+  const size_t elt = all.act == PALU_F32 ? 4 : 2;
+  for (int u0 = 0; u0 < all.batch; u0 += p.units) {
+    palu::DecodeArgs a = all;
+    a.batch = all.batch - u0 < p.units ? all.batch - u0 : p.units;
+    a.qn = 1;
+    a.S = 1;
+    a.walk_ctas = p.ctas;
+    char* at = reinterpret_cast<char*>(all.part);
+    a.cont = reinterpret_cast<float*>(at + p.part);
+    a.segments = reinterpret_cast<int2*>(at + p.part + p.cont);
+    a.fused_q = at + p.part + p.cont + p.segments;
+    a.q = static_cast<const char*>(all.q) + (size_t)u0 * all.q_bstride * elt;
+    a.q_pos += u0;
+    a.out = static_cast<char*>(all.out) + (size_t)u0 * all.o_bstride * elt;
+    if (a.lse != nullptr) a.lse += (size_t)u0 * all.lse_bstride;
+    a.page_list += (size_t)u0 * a.G * a.list_len;
+    a.page_counts += (size_t)u0 * a.G;
+    a.page_table += (size_t)(u0 / a.queries) * a.max_pages;
+    a.seq_lens += u0 / a.queries;
+    cudaError_t e = kind == 3 ? palu::launch_decode_fused(a, st) : palu::launch_decode_tc(a, st);
+    if (e != cudaSuccess) return e;
+    e = palu::launch_combine(a, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const int32_t* q_pos,
                          const void* zk_pool, const void* zv_pool, const void* zk_scales, const void* zv_scales,
@@ -422,7 +498,7 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
   if (num_splits > walk) return PALU_ERR_INVALID_ARG;
   if (sparse && (long long)batch * Q > 65535) return PALU_ERR_UNSUPPORTED;
   size_t fused_off = 0;
-  const size_t need = sparse ? decode_workspace(L, batch * Q, 1, walk, num_splits, &fused_off)
+  const size_t need = sparse ? pages_workspace(L, batch, Q, walk, num_splits)
                              : decode_workspace(L, batch, Q, max_pages, num_splits, &fused_off);
   if (workspace == nullptr || workspace_bytes < need) return PALU_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
@@ -477,6 +553,10 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
     a.page_counts = sparse->counts;
     a.list_len = sparse->len;
     a.queries = Q;
+    a.q = q;
+    a.q_pos = q_pos;
+    a.out = out;
+    a.lse = lse;
     a.batch = batch * Q;
     a.q_bstride = a.o_bstride = qrow;
     a.qpos_bstride = 1;
@@ -488,7 +568,7 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
   for (int c = 0; c < L.nset; ++c) {
     const palu_config cc = set_cfg(L, c);
     const int kind = kernel_kind(&cc);
-    a.S = run_S(&cc, kind, a.batch, walk, num_splits, pass_queries(kind, Q));
+    a.S = run_S(&cc, kind, a.batch, walk, num_splits, sparse ? 1 : pass_queries(kind, Q));
     a.r_k = cc.rank_k;
     a.r_v = cc.rank_v;
     a.k_row = palu::latent_row_bytes(a.lat, a.r_k);
@@ -499,8 +579,13 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
     a.bk_box = a.r_k;
     for (int i = 0; i < a.gm.n; ++i)
       if (a.gm.rk[i] != a.r_k) a.bk_box = 64;   // mixed key ranks: boxes of 64 rows
+    if (sparse && kind != 1) {
+      const cudaError_t e = walk_set(a, walk_plan(&cc, kind, batch, sparse->queries, walk), kind, st);
+      if (e != cudaSuccess) return cuda_status(e);
+      continue;
+    }
     for (int j = 0; j < Q; j += a.qn) {
-      a.qn = pass_queries(kind, Q - j);   // queries j .. j + qn - 1 of every sequence
+      a.qn = sparse ? 1 : pass_queries(kind, Q - j);   // queries j .. j + qn - 1 of every sequence
       a.q = static_cast<const char*>(q) + (size_t)j * qrow * elt;
       a.q_pos = q_pos + j;
       a.out = static_cast<char*>(out) + (size_t)j * qrow * elt;
@@ -656,7 +741,7 @@ palu_status palu_decode_pages_workspace_size(const palu_config* cfg, const int32
       num_queries > kMaxQueries)
     return PALU_ERR_INVALID_ARG;
   if ((long long)batch * num_queries > 65535) return PALU_ERR_UNSUPPORTED;
-  *bytes = decode_workspace(L, batch * num_queries, 1, list_len, num_splits, nullptr);
+  *bytes = pages_workspace(L, batch, num_queries, list_len, num_splits);
   return PALU_OK;
 }
 
@@ -676,6 +761,7 @@ palu_status palu_decode_attn_pages(const palu_config* cfg, const int32_t* ranks_
   lists.list = page_list;
   lists.counts = page_counts;
   lists.len = list_len;
+  lists.queries = num_queries;
   return decode_layer(L, batch, num_queries, q, q_pos, zk_pool, zv_pool, zk_scales, zv_scales, pos_pool, page_table,
                       max_pages, seq_lens, num_pages, B_k, B_v, out, lse, workspace, workspace_bytes, num_splits,
                       stream, &lists);

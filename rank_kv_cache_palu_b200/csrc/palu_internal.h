@@ -12,6 +12,7 @@ namespace palu {
 
 constexpr int kMaxHalfDim = 64;  // head_dim <= 128
 constexpr int kMaxGroups = 64;   // head groups per layer
+constexpr int kPartHead = 8;     // floats ahead of a[r_v] in a segment's partial: m, l of four warps
 
 // Where the head groups a launch covers keep their latents.  All groups of a
 // launch share one rank pair (r_k, r_v); a layer whose groups have different
@@ -75,6 +76,10 @@ struct DecodeArgs {
   const int32_t* page_list;   // NULL: every page
   const int32_t* page_counts;
   int list_len, queries;
+  int walk_ctas;              // tensor-core and fused kernels: CTAs per block column (see pages_walk.cuh)
+  float* cont;                // [walk_ctas][gm.n·gs][r_v + kPartHead] continuation partials (part: the main ones,
+                              // [batch][gm.n·gs][r_v + kPartHead])
+  int2* segments;             // [batch][gm.n]: first continuation CTA of a list and how many there are
 };
 
 // Phase-trace buffer set by palu_debug_trace (NULL: off).
@@ -115,16 +120,11 @@ struct TimeoutTest {
 };
 TimeoutTest timeout_test_setting();
 
-// Logical pages one CTA of a sparse step walks: entries [e0, e1) of its list.
-struct ListRange {
-  const int32_t* list;   // entry e0 of the list
-  int n, T, npg, sb;     // entries, cached tokens, pages and index of the sequence
-  bool ragged_last;      // the last entry is the sequence's partial last page
-};
-
 // CUDA-core kernels (any supported dtype; the only path for float32).
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t st);
+// The merge after a walk over page lists (DecodeArgs::segments set); launch_combine calls it.
+cudaError_t launch_pages_combine(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_compress_simt(const CompressArgs& a, cudaStream_t st);
 
 // Page bounds and page selection (see palu_page_bounds, palu_select_pages).

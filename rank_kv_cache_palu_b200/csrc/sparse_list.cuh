@@ -1,5 +1,5 @@
-// Page lists of the sparse decode step (palu_decode_attn_pages), shared by its
-// tensor-core, fused and CUDA-core kernels.
+// Page lists of the sparse decode step (palu_decode_attn_pages) for the CUDA-core
+// split kernel; the tensor-core kernels walk them as pages_walk.cuh lays out.
 #pragma once
 
 #include "palu_common.cuh"
@@ -8,10 +8,12 @@
 namespace palu {
 namespace {
 
-// Raw page-table entry of logical page lp; -1 where lp is outside the sequence.
-__device__ __forceinline__ int list_page(const DecodeArgs& a, const ListRange& lr, int lp) {
-  return lp >= 0 && lp < lr.npg ? a.page_table[(size_t)lr.sb * a.max_pages + lp] : -1;
-}
+// Logical pages one CTA walks: entries [e0, e1) of its list.
+struct ListRange {
+  const int32_t* list;   // entry e0 of the list
+  int n, T, npg, sb;     // entries, cached tokens, pages and index of the sequence
+  bool ragged_last;      // the last entry is the sequence's partial last page
+};
 
 // This CTA's share (split blockIdx.x of a.S) of the list of virtual sequence vb
 // and model group g.  Thread i checks every blockDim-th entry: lists ascend and
