@@ -257,13 +257,14 @@ _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 class _Args:
     """Checks the tensors of one call and gives their addresses.  The workspace names the device."""
 
-    __slots__ = ("where", "device")
+    __slots__ = ("where", "device", "wrong")
 
     def __init__(self, where: str, workspace):
         if not isinstance(workspace, torch.Tensor):
             raise TypeError(f"{where}: workspace must be a torch.Tensor")
         self.where = where
         self.device = workspace.get_device()
+        self.wrong = None            # what is not where the workspace is (told once shapes and types are known good)
 
     def __call__(self, name, t, dtype, shape=None):
         if t is None:
@@ -271,9 +272,9 @@ class _Args:
         if (isinstance(t, torch.Tensor) and t.get_device() == self.device >= 0 and t.is_contiguous() and
                 (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
             return t.data_ptr()
-        return self._refuse(name, t, dtype, shape)
+        return self._elsewhere(name, self._sound(name, t, dtype, shape))
 
-    def _refuse(self, name, t, dtype, shape):
+    def _sound(self, name, t, dtype, shape):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{self.where}: {name} must be a torch.Tensor or None")
         if dtype is not None and t.dtype is not dtype:
@@ -282,14 +283,14 @@ class _Args:
             raise ValueError(f"{self.where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{self.where}: {name} must be contiguous")
-        return self._elsewhere(name, t)
+        return t
 
     def _elsewhere(self, name, t):
         if t.numel() == 0:
             return None
-        if not t.is_cuda:
-            raise ValueError(f"{self.where}: {name} must live in CUDA device memory")
-        raise ValueError(f"{self.where}: {name} is on {t.device}, the workspace on device {self.device}")
+        self.wrong = f"{name} must live in CUDA device memory" if not t.is_cuda else \
+            f"{name} is on {t.device}, the workspace on device {self.device}"
+        return None
 
     def rows(self, name, t, dtype, shape):
         """Address and row stride of [batch][rows][width] probabilities; rows may be padded."""
@@ -310,7 +311,9 @@ class _Args:
 
     def call(self, fn, *args, stream=None):
         if self.device < 0:
-            raise ValueError(f"{self.where}: workspace must live in CUDA device memory")
+            self.wrong = "workspace must live in CUDA device memory"
+        if self.wrong is not None:
+            raise ValueError(f"{self.where}: {self.wrong}")
         if self.device == torch.cuda.current_device():
             status = fn(*args, self._stream(stream))
         else:
