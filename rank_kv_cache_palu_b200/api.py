@@ -254,6 +254,9 @@ def palu_decode_attn_noalloc(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_sca
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
+_get_device, _is_contiguous, _data_ptr = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+
+
 class _Args:
     """Checks the tensors of one call and gives their addresses.  The workspace names the device."""
 
@@ -273,6 +276,18 @@ class _Args:
                 (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
             return t.data_ptr()
         return self._elsewhere(name, self._sound(name, t, dtype, shape))
+
+    def take(self, names, tensors, dtypes, shapes):
+        """Addresses of several tensors: what __call__ does for each, in a few passes over all of them
+        (half the host time of a small call is spent on these checks)."""
+        try:
+            if (list(map(_get_device, tensors)) == [self.device] * len(tensors) and self.device >= 0 and
+                    all(map(_is_contiguous, tensors)) and [t.dtype for t in tensors] == dtypes and
+                    [t.shape for t in tensors] == shapes):
+                return list(map(_data_ptr, tensors))
+        except TypeError:
+            pass
+        return [self(*a) for a in zip(names, tensors, dtypes, shapes)]
 
     def _sound(self, name, t, dtype, shape):
         if not isinstance(t, torch.Tensor):
@@ -348,16 +363,15 @@ def palu_plan_append(page_size: int, num_new, seq_lens, page_table, free_pages, 
     """
     A = _Args("palu_plan_append", workspace)
     batch, max_pages = page_table.shape
-    one = (batch,)
-    A.call(load().palu_plan_append, page_size, batch, max_pages, free_pages.numel(), slot_mapping.numel(),
-           A("num_new", num_new, _I32, one), A("seq_lens", seq_lens, _I32, one), A("page_table", page_table, _I32),
-           A("free_pages", free_pages, _I32, (free_pages.numel(),)), A("num_free", num_free, _I32, (1,)),
-           A("slot_mapping", slot_mapping, _I32, (slot_mapping.numel(),)),
-           A("positions", positions, _I32, (slot_mapping.numel(),)),
+    one, rows = (batch,), (slot_mapping.numel(),)
+    state = A.take(_PLAN, (num_new, seq_lens, page_table, free_pages, num_free, slot_mapping, positions), [_I32] * 7,
+                   [one, one, (batch, max_pages), (free_pages.numel(),), (1,), rows, rows])
+    A.call(load().palu_plan_append, page_size, batch, max_pages, free_pages.numel(), rows[0], *state,
            A("row_starts", row_starts, _I32, (batch + 1,)), A("taken", taken, _I32, one),
            A("workspace", workspace, None), workspace.numel() * workspace.element_size(), stream=stream)
 
 
+_PLAN = ("num_new", "seq_lens", "page_table", "free_pages", "num_free", "slot_mapping", "positions")
 _PROBS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
@@ -383,14 +397,16 @@ def palu_verify_drafts(target_probs, draft_probs, draft_tokens, draft_lens, u_ac
     p, p_ld = A.rows("target_probs", target_probs, target_probs.dtype, (batch, n, vocab))
     q, q_ld = (None, 0) if draft_probs is None or D == 0 else \
         A.rows("draft_probs", draft_probs, target_probs.dtype, (batch, D, vocab))
+    drafts, uniform, sample, out, accepted = A.take(
+        _VERIFY, (draft_tokens, u_accept, u_sample, tokens, num_accepted), [_I32, _F32, _F32, _I32, _I32],
+        [(batch, D), (batch, D), one, (batch, n), one])
     A.call(load().palu_verify_drafts, _PROBS[target_probs.dtype], batch, D, vocab, p, p_ld, q, q_ld,
-           A("draft_tokens", draft_tokens, _I32, (batch, D)), A("draft_lens", draft_lens, _I32, one),
-           A("u_accept", u_accept, _F32, (batch, D)), A("u_sample", u_sample, _F32, one),
-           A("tokens", tokens, _I32, (batch, n)), A("num_accepted", num_accepted, _I32, one),
+           drafts, A("draft_lens", draft_lens, _I32, one), uniform, sample, out, accepted,
            A("rollback", rollback, _I32, one), A("workspace", workspace, None),
-           workspace.numel() * workspace.element_size(), stream=stream)
+           workspace.nbytes, stream=stream)
 
 
+_VERIFY = ("draft_tokens", "u_accept", "u_sample", "tokens", "num_accepted")
 _ACT_TORCH = {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
 
 
@@ -418,12 +434,14 @@ def _factor(A, name, B, cfg, ranks):
     """B_k or B_v: the groups' [rank][group width] blocks, back to back."""
     if B.numel() != sum(ranks) * cfg.group_size * cfg.head_dim:
         raise ValueError(f"{A.where}: {name} must hold {sum(ranks)} rows of {cfg.group_size * cfg.head_dim}")
-    return A(name, B, _ACT_TORCH[cfg.act_dtype])
+    return A(name, B, _ACT_TORCH.get(cfg.act_dtype))
 
 
 def _pool(A, name, pool, num_pages, page_bytes):
     """A cache pool that holds at least num_pages pages."""
-    if pool is not None and pool.numel() * pool.element_size() < num_pages * page_bytes:
+    if pool is None:
+        return None
+    if pool.nbytes < num_pages * page_bytes:
         raise ValueError(f"{A.where}: {name} holds fewer than {num_pages} pages")
     return A(name, pool, None)
 
@@ -441,8 +459,8 @@ def palu_page_bounds(cfg: PaluConfig, first, zk_pool, zk_scales, pos_pool, page_
            _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
            _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size), A("page_table", page_table, _I32), max_pages,
            A("seq_lens", seq_lens, _I32, (batch,)), num_pages, _factor(A, "B_k", B_k, cfg, rk),
-           A("bounds", bounds, _ACT_TORCH[cfg.act_dtype]), A("workspace", workspace, None),
-           workspace.numel() * workspace.element_size(), stream=stream)
+           A("bounds", bounds, _ACT_TORCH.get(cfg.act_dtype)), A("workspace", workspace, None),
+           workspace.nbytes, stream=stream)
 
 
 def palu_select_workspace_size(cfg: PaluConfig, batch: int, num_queries: int, max_pages: int) -> int:
@@ -461,14 +479,19 @@ def palu_select_pages(cfg: PaluConfig, q, q_pos, bounds, pos_pool, page_table, s
     G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
     if bounds.numel() < _bounds_numel(cfg, num_pages):
         raise ValueError(f"palu_select_pages: bounds holds fewer than {num_pages} pages")
-    A.call(load().palu_select_pages, ctypes.byref(cfg), batch, Q,
-           A("q", q, _ACT_TORCH[cfg.act_dtype], (batch, Q, cfg.num_heads, cfg.head_dim)), A("q_pos", q_pos, _I32),
-           A("bounds", bounds, _ACT_TORCH[cfg.act_dtype]), A("pos_pool", pos_pool, _I32),
-           A("page_table", page_table, _I32, (batch, max_pages)), max_pages, A("seq_lens", seq_lens, _I32, (batch,)),
-           num_pages, num_first, num_last, keep, A("page_list", page_list, _I32, (batch, Q, G, keep)),
-           A("page_counts", page_counts, _I32, (batch, Q, G)),
+    query, at, table, lens, lists, counts = A.take(
+        _SELECT, (q, q_pos, page_table, seq_lens, page_list, page_counts),
+        [_ACT_TORCH.get(cfg.act_dtype), _I32, _I32, _I32, _I32, _I32],
+        [(batch, Q, cfg.num_heads, cfg.head_dim), (batch, Q), (batch, max_pages), (batch,), (batch, Q, G, keep),
+         (batch, Q, G)])
+    A.call(load().palu_select_pages, ctypes.byref(cfg), batch, Q, query, at,
+           A("bounds", bounds, _ACT_TORCH.get(cfg.act_dtype)), A("pos_pool", pos_pool, _I32), table, max_pages, lens,
+           num_pages, num_first, num_last, keep, lists, counts,
            A("page_scores", page_scores, _F32, (batch, Q, G, keep)), A("workspace", workspace, None),
-           workspace.numel() * workspace.element_size(), stream=stream)
+           workspace.nbytes, stream=stream)
+
+
+_SELECT = ("q", "q_pos", "page_table", "seq_lens", "page_list", "page_counts")
 
 
 def palu_decode_pages_workspace_size(cfg: PaluConfig, batch: int, num_queries: int, list_len: int,
@@ -488,19 +511,22 @@ def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scale
     A = _Args("palu_decode_attn_pages", workspace)
     batch, Q = q_pos.shape
     G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
-    rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _ACT_TORCH[cfg.act_dtype]
+    rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _ACT_TORCH.get(cfg.act_dtype)
     rk, rv = ranks_k or (cfg.rank_k,) * G, ranks_v or (cfg.rank_v,) * G
     (kb, ksb), (vb, vsb) = _page_bytes(cfg, rk), _page_bytes(cfg, rv)
-    A.call(load().palu_decode_attn_pages, ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch, Q,
-           A("q", q, act, rows), A("q_pos", q_pos, _I32), _pool(A, "zk_pool", zk_pool, num_pages, kb),
-           _pool(A, "zv_pool", zv_pool, num_pages, vb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
-           _pool(A, "zv_scales", zv_scales, num_pages, vsb),
-           _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size),
-           A("page_table", page_table, _I32, (batch, max_pages)), max_pages, A("seq_lens", seq_lens, _I32, (batch,)),
-           A("page_list", page_list, _I32, (batch, Q, G, keep)), A("page_counts", page_counts, _I32, (batch, Q, G)),
-           keep, num_pages, _factor(A, "B_k", B_k, cfg, rk), _factor(A, "B_v", B_v, cfg, rv), A("out", out, act, rows),
+    query, at, table, lens, lists, counts, result = A.take(
+        _ATTEND, (q, q_pos, page_table, seq_lens, page_list, page_counts, out), [act, _I32, _I32, _I32, _I32, _I32, act],
+        [rows, (batch, Q), (batch, max_pages), (batch,), (batch, Q, G, keep), (batch, Q, G), rows])
+    A.call(load().palu_decode_attn_pages, ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch, Q, query, at,
+           _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zv_pool", zv_pool, num_pages, vb),
+           _pool(A, "zk_scales", zk_scales, num_pages, ksb), _pool(A, "zv_scales", zv_scales, num_pages, vsb),
+           _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size), table, max_pages, lens, lists, counts, keep,
+           num_pages, _factor(A, "B_k", B_k, cfg, rk), _factor(A, "B_v", B_v, cfg, rv), result,
            A("lse", lse, _F32, rows[:3]), A("workspace", workspace, None),
-           workspace.numel() * workspace.element_size(), num_splits, stream=stream)
+           workspace.nbytes, num_splits, stream=stream)
+
+
+_ATTEND = ("q", "q_pos", "page_table", "seq_lens", "page_list", "page_counts", "out")
 
 
 def palu_get_device_status(workspace, stream=None) -> tuple[int, int]:
