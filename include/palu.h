@@ -417,7 +417,7 @@ palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int
  * scores computed in float64 (page_scores are float32 sums, within 2^-20 Σ_c
  * (|q_c| + |q_pair(c)|) |v_c| of them, v_c the bound taken); of equal scores
  * the lower page wins; a head's sum that is not a number counts as -inf.
- * batch·G <= PALU_SELECT_MAX_LISTS, max_pages <= PALU_SELECT_MAX_PAGES and
+ * batch·num_queries·G <= PALU_SELECT_MAX_LISTS, max_pages <= PALU_SELECT_MAX_PAGES and
  * group_size·head_dim <= 8192 (PALU_ERR_UNSUPPORTED above). */
 #define PALU_SELECT_MAX_LISTS 65536
 #define PALU_SELECT_MAX_PAGES 32768

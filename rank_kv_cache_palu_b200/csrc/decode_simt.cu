@@ -9,7 +9,6 @@
 
 #include "palu_common.cuh"
 #include "palu_internal.h"
-#include "sparse_list.cuh"
 
 namespace palu {
 namespace {
@@ -45,9 +44,7 @@ __device__ __forceinline__ SplitRange split_range(int T, int P, int S, int s) {
   return r;
 }
 
-// SPARSE: the range runs over the tokens of the listed pages, t counting them; map() gives a
-// token's place in the sequence.
-template <int ACT, int LAT, bool SPARSE>
+template <int ACT, int LAT>
 __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__ DecodeArgs a) {
   using TA = typename Dt<ACT>::T;
   extern __shared__ float smem[];
@@ -68,25 +65,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
   float* sc = kt + kTT * d_h;             // [kTT] scores
   int* tpos = reinterpret_cast<int*>(sc + kTT);  // [kTT] positions
 
-  ListRange lr{};
-  SplitRange rg;
-  int row_b = b;                          // page-table row
-  if constexpr (SPARSE) {
-    lr = list_range(a, b, a.gm.g[gi], st);
-    row_b = lr.sb;
-    const int last = lr.n > 0 ? lr.list[lr.n - 1] : 0;
-    // a partial last page ends the list
-    rg = SplitRange{0, lr.n * a.P - (lr.ragged_last ? min(a.P, max(0, (last + 1) * a.P - lr.T)) : 0)};
-  } else {
-    rg = split_range(checked_len(a, b, st), a.P, a.S, s);
-  }
-  auto map = [&](int t) -> int {          // place in the sequence; -1: a page that the sequence does not have
-    if constexpr (SPARSE) {
-      const int lp = lr.list[t / a.P];
-      return lp >= 0 && lp < lr.npg ? lp * a.P + t % a.P : -1;
-    }
-    return t;
-  };
+  const int T = checked_len(a, b, st);
+  const SplitRange rg = split_range(T, a.P, a.S, s);
 
   // Rotated query, with the softmax scale folded in.
   const TA* qh = reinterpret_cast<const TA*>(a.q) + (size_t)b * a.q_bstride + (size_t)h * d_h;
@@ -110,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
   const uint8_t* zv_base = a.gm.zv[gi];
   const uint8_t* zks_base = a.gm.zks[gi];
   const uint8_t* zvs_base = a.gm.zvs[gi];
-  const int32_t* ptab = a.page_table + (size_t)row_b * a.max_pages;
+  const int32_t* ptab = a.page_table + (size_t)b * a.max_pages;
 
   for (int t0 = rg.t_begin; t0 < rg.t_end; t0 += kTT) {
     const int nt = min(kTT, rg.t_end - t0);
@@ -119,8 +99,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
     if (tid < kTT) {
       int pv = 0;
       if (tid < nt) {
-        const int t = map(t0 + tid);
-        int page = t >= 0 ? ptab[t / a.P] : -1;
+        const int t = t0 + tid;
+        int page = ptab[t / a.P];
         if (page < 0 || page >= a.num_pages) page = -1;
         pv = (a.pos_pool != nullptr && page >= 0) ? a.pos_pool[(size_t)page * a.P + t % a.P] : t;
       }
@@ -130,8 +110,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
       const int tt = e / r_k, j = e % r_k;
       float v = 0.f;
       if (tt < nt) {
-        const int t = map(t0 + tt);
-        const int page = t >= 0 ? ptab[t / a.P] : -1;
+        const int t = t0 + tt;
+        const int page = ptab[t / a.P];
         if (page < 0 || page >= a.num_pages) {
           report(st, PALU_ERR_DEVICE_BOUNDS, 2000000 + b);
         } else {
@@ -148,8 +128,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const __grid_constant__
       const int tt = e / a.r_v, j = e % a.r_v;
       float v = 0.f;
       if (tt < nt) {
-        const int t = map(t0 + tt);
-        const int page = t >= 0 ? ptab[t / a.P] : -1;
+        const int t = t0 + tt;
+        const int page = ptab[t / a.P];
         if (page >= 0 && page < a.num_pages) {
           v = load_latent<LAT, ACT>(zv_base + (size_t)page * a.gm.v_page, t % a.P, a.P,
                                     LAT == PALU_INT4 ? zvs_base + (size_t)page * a.gm.vs_page +
@@ -329,7 +309,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
 template <int ACT, int LAT>
 cudaError_t launch_split_t(const DecodeArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(float) * (a.d_h + kTT * (a.r_k + a.r_v + a.d_h) + kTT) + sizeof(int) * kTT;
-  auto kern = a.page_list != nullptr ? split_kernel<ACT, LAT, true> : split_kernel<ACT, LAT, false>;
+  auto kern = split_kernel<ACT, LAT>;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -343,6 +323,7 @@ cudaError_t launch_split_t(const DecodeArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st) {
+  if (a.page_list != nullptr) return launch_decode_pages_simt(a, st);
   if (a.act == PALU_F32 && a.lat == PALU_F32) return launch_split_t<PALU_F32, PALU_F32>(a, st);
   if (a.act == PALU_F16 && a.lat == PALU_F16) return launch_split_t<PALU_F16, PALU_F16>(a, st);
   if (a.act == PALU_BF16 && a.lat == PALU_BF16) return launch_split_t<PALU_BF16, PALU_BF16>(a, st);

@@ -24,6 +24,7 @@
 //
 // Every other shape, and float32, takes the CUDA-core kernel.
 #include "decode_tc_kernel.cuh"
+#include "simt_keys.cuh"
 
 namespace palu {
 namespace {
@@ -82,69 +83,69 @@ template <> struct Out<PALU_BF16> {
 };
 
 // ---------------------------------------------------------------- CUDA cores
-constexpr int kSimtThreads = 128;
-constexpr int kTT = 16;   // tokens per tile
-
+// One CTA per (page, head): the keys of the page's tokens in passes of 128 (64 for
+// heads wider than 64; simt_keys.cuh), rotated and reduced in the threads, then over
+// the token runs.
 template <int ACT, int LAT>
-__global__ void __launch_bounds__(kSimtThreads) bounds_simt_kernel(const __grid_constant__ BoundsArgs a) {
+__global__ void __launch_bounds__(kKeyThreads) bounds_simt_kernel(const __grid_constant__ BoundsArgs a) {
   using TA = typename Dt<ACT>::T;
-  extern __shared__ float smem_f[];
+  extern __shared__ __align__(16) float zt[];
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int g = h / a.gs, jh = h % a.gs;
-  const int r_k = a.gm.rk[g], d_h = a.d_h, half = d_h / 2;
-  float* zt = smem_f;               // [kTT][r_k]
-  float* kt = zt + kTT * r_k;       // [kTT][d_h]
+  const int r_k = a.gm.rk[g], half = a.d_h / 2;
+  const int lanes = key_lanes(half), tokens = key_tokens(half);
+  const int i = tid % lanes, run = tid / lanes;
   const int T = tokens_of(a, b, tid == 0 && blockIdx.x == 0 && h == 0);
   const int npg = (T + a.P - 1) / a.P;
-  const TA* Bk = reinterpret_cast<const TA*>(a.Bk) + (size_t)a.gm.k_row0[g] * a.W + jh * d_h;
-  const long long ks_row = int4_scale_row(r_k);
+  const TA* Bk = reinterpret_cast<const TA*>(a.Bk) + (size_t)a.gm.k_row0[g] * a.W + jh * a.d_h;
   for (int lp = first_page(a, b) + blockIdx.x; lp < npg; lp += gridDim.x) {
     const int page = a.page_table[(size_t)b * a.max_pages + lp];
     if (page < 0 || page >= a.num_pages) {
       if (tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 2000000 + b);
       continue;
     }
-    const int nv = min(a.P, T - lp * a.P);
+    const int rows = min(a.P, T - lp * a.P);
     const uint8_t* blk = a.gm.zk[g] + (size_t)page * a.gm.k_page;
     const uint8_t* sblk = LAT == PALU_INT4 ? a.gm.zks[g] + (size_t)page * a.gm.ks_page : nullptr;
-    float lo1 = INFINITY, hi1 = -INFINITY, lo2 = INFINITY, hi2 = -INFINITY;   // thread i < half: channels i, i + half
-    for (int t0 = 0; t0 < nv; t0 += kTT) {
-      const int nt = min(kTT, nv - t0);
-      __syncthreads();
-      for (int e = tid; e < kTT * r_k; e += kSimtThreads) {
-        const int tt = e / r_k, j = e - tt * r_k;
-        zt[e] = tt < nt ? load_latent<LAT, ACT>(blk, t0 + tt, a.P, sblk + (size_t)(t0 + tt) * ks_row, j) : 0.f;
-      }
-      __syncthreads();
-      for (int d = tid; d < d_h; d += kSimtThreads) {
-        float acc[kTT];
+    float lo1 = INFINITY, hi1 = -INFINITY, lo2 = INFINITY, hi2 = -INFINITY;   // channels i, i + half
+    for (int t0 = 0; t0 < rows; t0 += tokens) {
+      const int nt = min(tokens, rows - t0);
+      float k1[kKeyRun], k2[kKeyRun];
+      rebuild_keys<ACT, LAT>(blk, sblk, a.P, t0, nt, r_k, Bk, a.W, half, zt, k1, k2);
 #pragma unroll
-        for (int tt = 0; tt < kTT; ++tt) acc[tt] = 0.f;
-        for (int r = 0; r < r_k; ++r) {
-          const float bv = Dt<ACT>::to_f(Bk[(size_t)r * a.W + d]);
-#pragma unroll
-          for (int tt = 0; tt < kTT; ++tt) acc[tt] = fmaf(zt[tt * r_k + r], bv, acc[tt]);
-        }
-#pragma unroll
-        for (int tt = 0; tt < kTT; ++tt) kt[tt * d_h + d] = acc[tt];
-      }
-      __syncthreads();
-      if (tid < half) {
-        for (int tt = 0; tt < nt; ++tt) {
+      for (int t = 0; t < kKeyRun; ++t) {
+        const int tt = run * kKeyRun + t;
+        if (tt >= nt || i >= half) continue;
+        float v1 = k1[t], v2 = k2[t];
+        if (a.rope) {
           const int pos = a.pos_pool != nullptr ? a.pos_pool[(size_t)page * a.P + t0 + tt] : lp * a.P + t0 + tt;
-          const float k1 = kt[tt * d_h + tid], k2 = kt[tt * d_h + half + tid];
-          float c = 1.f, s = 0.f;
-          if (a.rope) rope_cs_accurate(pos, a.omega[tid], c, s);
-          const float v1 = a.rope ? k1 * c - k2 * s : k1, v2 = a.rope ? k2 * c + k1 * s : k2;
-          lo1 = fminf(lo1, v1);
-          hi1 = fmaxf(hi1, v1);
-          lo2 = fminf(lo2, v2);
-          hi2 = fmaxf(hi2, v2);
+          float c, s;
+          rope_cs_accurate(pos, a.omega[i], c, s);
+          v1 = k1[t] * c - k2[t] * s;
+          v2 = k2[t] * c + k1[t] * s;
         }
+        lo1 = fminf(lo1, v1);
+        hi1 = fmaxf(hi1, v1);
+        lo2 = fminf(lo2, v2);
+        hi2 = fmaxf(hi2, v2);
       }
     }
+    __syncthreads();   // the staging buffer takes the runs' results: [run][lo1, hi1, lo2, hi2][pair]
+    float* x = zt + run * 4 * lanes + i;
+    x[0] = lo1;
+    x[lanes] = hi1;
+    x[2 * lanes] = lo2;
+    x[3 * lanes] = hi2;
+    __syncthreads();
     if (tid < half) {
-      TA* o = reinterpret_cast<TA*>(a.bounds) + ((size_t)page * a.G + g) * 2 * a.W + jh * d_h + tid;
+      for (int w = 1; w < kKeyThreads / lanes; ++w) {
+        const float* y = zt + w * 4 * lanes + tid;
+        lo1 = fminf(lo1, y[0]);
+        hi1 = fmaxf(hi1, y[lanes]);
+        lo2 = fminf(lo2, y[2 * lanes]);
+        hi2 = fmaxf(hi2, y[3 * lanes]);
+      }
+      TA* o = reinterpret_cast<TA*>(a.bounds) + ((size_t)page * a.G + g) * 2 * a.W + jh * a.d_h + tid;
       o[0] = Out<ACT>::down(lo1);
       o[half] = Out<ACT>::down(lo2);
       o[a.W] = Out<ACT>::up(hi1);
@@ -155,17 +156,12 @@ __global__ void __launch_bounds__(kSimtThreads) bounds_simt_kernel(const __grid_
 
 template <int ACT, int LAT>
 cudaError_t launch_simt(const BoundsArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(float) * kTT * (a.max_rk + a.d_h);
-  auto kern = bounds_simt_kernel<ACT, LAT>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = sizeof(float) * key_stage_floats(a.d_h / 2);
   // pages of a sequence: enough CTAs for ~16 per SM, each stepping over the rest
   const long long rows = (long long)a.G * a.gs * a.batch;
   long long x = (16LL * 148 + rows - 1) / rows;
   x = x < 1 ? 1 : x > a.max_pages ? a.max_pages : x;
-  kern<<<dim3((int)x, a.G * a.gs, a.batch), kSimtThreads, smem, st>>>(a);
+  bounds_simt_kernel<ACT, LAT><<<dim3((int)x, a.G * a.gs, a.batch), kKeyThreads, smem, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }

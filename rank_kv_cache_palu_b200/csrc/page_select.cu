@@ -4,10 +4,10 @@
 //   score(page) = max_h Σ_c max(q'_h,c lo_c, q'_h,c hi_c),   q' = R(q_pos) q,
 // the larger product being q'·hi for q' >= 0 and q'·lo below.
 //
-// One CTA scores a run of pages of one (sequence, group).  A page's 2·W entries of a
-// group are contiguous (2 KB in the 7B shape): every warp streams its pages through
-// four slots of shared memory with bulk copies and sums two pages side by side.
-// Several queries read the bounds again (from L2).
+// One CTA scores a run of pages for one list (sequence, group, query).  A page's 2·W
+// entries of a group are contiguous (2 KB in the 7B shape): every warp streams its
+// pages through four slots of shared memory with bulk copies and sums two pages side
+// by side.  The CTAs of a step's other queries read the same bounds from L2.
 //
 // Which pages win is a whole number, so the order is that of the float64 scores.
 // Float64 sums for every page are bound by their conversions (16 a clock and SM) and
@@ -20,7 +20,7 @@
 // inside that band have to be told apart are their float64 scores taken (about one
 // list in a hundred with random boxes; every page where E is not finite).
 //
-// The last CTA of a (sequence, group) (a ticket) cuts the lists: scores become
+// The last CTA of a list (a ticket) cuts it: scores become
 // order-preserving keys; a histogram over the 8 bits below the highest bit in which
 // the keys differ finds the bin of the last kept page, and is repeated inside that
 // bin until at most 32 keys are left, which one warp ranks.  Pages are compacted in
@@ -56,7 +56,7 @@ struct SelectArgs {
   int32_t* counts;
   float* scores_out;
   DevStatus* st;
-  unsigned* tickets;     // [batch·G]
+  unsigned* tickets;     // [batch·G·Q]
   double* exact;         // [batch][G][Q][max_pages]: float64 scores where they are needed
   float* scores;         // [batch][G][Q][max_pages]
   float* errs;           // [batch][G][Q][chunks]: what E is taken from
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
   __shared__ int is_last;
   __shared__ float werr[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = blockIdx.y, b = blockIdx.z;
+  const int g = blockIdx.y / a.Q, j = blockIdx.y % a.Q, b = blockIdx.z;   // one (sequence, group, query): a list
   const int cap = a.max_pages * a.P;
   const int width = a.gs * a.d_h;
   float* qr = smem;
@@ -188,24 +188,22 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
   const int my_lp = p0 + lane * kWarps + warp;      // lane k: the warp's k-th page of the chunk
   int my_page = lane < a.chunk / kWarps && my_lp < a.max_pages ? a.page_table[(size_t)b * a.max_pages + my_lp] : -1;
   const int half = a.d_h / 2;
-  int qpos = a.q_pos[(size_t)b * a.Q];
-  auto query = [&](int j) {
-    return static_cast<const T*>(a.q) + (((size_t)b * a.Q + j) * a.H + (size_t)g * a.gs) * a.d_h;
-  };
+  const int qpos = a.q_pos[(size_t)b * a.Q + j];
+  const T* q = static_cast<const T*>(a.q) + (((size_t)b * a.Q + j) * a.H + (size_t)g * a.gs) * a.d_h;
   const int h_first = tid / half, f_first = tid - h_first * half;
   T x1{}, x2{};
   if (h_first < a.gs) {
-    x1 = query(0)[h_first * a.d_h + f_first];
-    x2 = query(0)[h_first * a.d_h + half + f_first];
+    x1 = q[h_first * a.d_h + f_first];
+    x2 = q[h_first * a.d_h + half + f_first];
   }
   if (T_ < 0 || T_ > cap) {
-    if (blockIdx.x == 0 && g == 0 && tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 1000000 + b);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 1000000 + b);
     T_ = T_ < 0 ? 0 : cap;
   }
   const int npg = (T_ + a.P - 1) / a.P;
   const int p1 = min(npg, p0 + a.chunk);
   const T* bounds = static_cast<const T*>(a.bounds);
-  const size_t unit = ((size_t)b * a.G + g) * a.Q;
+  const size_t unit = ((size_t)b * a.G + g) * a.Q + j;
   float* out = a.scores + unit * a.max_pages;
   float* errs = a.errs + unit * gridDim.x;
 
@@ -242,15 +240,10 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
     for (int s = 0; s < kSlots; ++s) issue(s);
   }
 
-  for (int j = 0; j < a.Q && p0 < p1; ++j) {
-    const T* q = query(j);
-    if (j > 0) {
-      __syncthreads();   // the previous query is done with qr
-      qpos = a.q_pos[(size_t)b * a.Q + j];
-    }
+  if (p0 < p1) {
     for (int i = tid; i < a.gs * half; i += kThreads) {
       const int h = i / half, f = i - h * half;
-      if (i >= kThreads || j > 0) {
+      if (i >= kThreads) {
         x1 = q[h * a.d_h + f];
         x2 = q[h * a.d_h + half + f];
       }
@@ -262,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
       qn[h * a.d_h + f] = qn[h * a.d_h + half + f] = fabsf(u) + fabsf(w);
     }
     __syncthreads();
-    float* mine = out + (size_t)j * a.max_pages + p0 + warp;
+    float* mine = out + p0 + warp;
     float err = 0.f;   // what E is taken from, over this warp's pages
     if constexpr (VEC) {
       // lanes_h lanes per head (4, 8 or 16), heads_w heads per pass
@@ -286,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
 #pragma unroll
           for (int w = 0; w < Box<DT>::kWords; ++w) top[u][w] = 0u;
         }
-        if (j + h0 > 0) {
+        if (h0 > 0) {
 #pragma unroll
           for (int s = 0; s < kSlots; ++s) issue(s);
         }
@@ -364,21 +357,21 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
     __syncthreads();
     if (tid == 0) {
       for (int w = 1; w < kWarps; ++w) err = fmaxf(err, werr[w]);
-      errs[(size_t)j * gridDim.x + blockIdx.x] = err;
+      errs[blockIdx.x] = err;
     }
   }
 
   __threadfence();   // every lane that wrote scores
   __syncthreads();
   if (gridDim.x > 1) {
-    if (tid == 0) is_last = atomicAdd(&a.tickets[(size_t)b * a.G + g], 1u) == gridDim.x - 1;
+    if (tid == 0) is_last = atomicAdd(&a.tickets[unit], 1u) == gridDim.x - 1;
     __syncthreads();
     if (!is_last) return;
     __threadfence();
-    if (tid == 0) a.tickets[(size_t)b * a.G + g] = 0;
+    if (tid == 0) a.tickets[unit] = 0;
   }
 
-  // ---- cut the list of each query
+  // ---- cut the list
   unsigned* keys = reinterpret_cast<unsigned*>(region);
   __shared__ unsigned hist[256];
   __shared__ unsigned wlo[kWarps], whi[kWarps], few[32];
@@ -423,253 +416,248 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
     }
     __syncthreads();
   };
-  for (int j = 0; j < a.Q; ++j) {
-    const int seen = min(npg, pages_seen(a, T_, a.q_pos[(size_t)b * a.Q + j]));
-    const int first = min(a.n_first, seen), tail = max(first, seen - a.n_last);   // kept: [0, first) and [tail, seen)
-    const int m = min(a.K, seen);
-    const int want = m - (first + seen - tail);      // pages to keep among [first, tail)
-    const float* sc = out + (size_t)j * a.max_pages;
-    double* exact = a.exact + (unit + j) * a.max_pages;
-    const size_t li = ((size_t)b * a.Q + j) * a.G + g;
+  const int seen = min(npg, pages_seen(a, T_, qpos));
+  const int first = min(a.n_first, seen), tail = max(first, seen - a.n_last);   // kept: [0, first) and [tail, seen)
+  const int m = min(a.K, seen);
+  const int want = m - (first + seen - tail);      // pages to keep among [first, tail)
+  const float* sc = out;
+  double* exact = a.exact + unit * a.max_pages;
+  const size_t li = ((size_t)b * a.Q + j) * a.G + g;
 
-    // pages [first, tail) are in with a key of at least in_key; those with a key in [band_key,
-    // in_key) where their float64 key lies above thr, or equals it and they are among the first `ties`
-    unsigned in_key = ~0u, band_key = ~0u;
-    unsigned long long thr = 0;
-    int ties = 0;
-    if (want > 0 && want == tail - first) {
-      in_key = 0;
-    } else if (want > 0) {
-      unsigned lo = ~0u, hi = 0;
-      float err = 0.f;
-      for (int i = first + tid; i < tail; i += kThreads) {
-        const unsigned k = key_of(__ldcg(sc + i));
-        keys[i] = k;
-        lo = min(lo, k);
-        hi = max(hi, k);
+  // pages [first, tail) are in with a key of at least in_key; those with a key in [band_key,
+  // in_key) where their float64 key lies above thr, or equals it and they are among the first `ties`
+  unsigned in_key = ~0u, band_key = ~0u;
+  unsigned long long thr = 0;
+  int ties = 0;
+  if (want > 0 && want == tail - first) {
+    in_key = 0;
+  } else if (want > 0) {
+    unsigned lo = ~0u, hi = 0;
+    float err = 0.f;
+    for (int i = first + tid; i < tail; i += kThreads) {
+      const unsigned k = key_of(__ldcg(sc + i));
+      keys[i] = k;
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
+    for (int c = tid; c < a.chunks; c += kThreads)
+      if (c * a.chunk < npg) err = fmaxf(err, __ldcg(errs + c));
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    err = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(err)));   // err >= 0
+    if (lane == 0) {
+      wlo[warp] = lo;
+      whi[warp] = hi;
+      werr[warp] = err;
+    }
+    hist[tid] = 0;
+    if (tid == 0) few_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      lo = min(lo, wlo[w]);
+      hi = max(hi, whi[w]);
+      err = fmaxf(err, werr[w]);
+    }
+    // the key of the want-th page from the top: keys in [base, base + 2^bits) still compete
+    int need = want;
+    int bits = lo == hi ? 0 : 32 - __clz((int)(lo ^ hi));
+    unsigned base = bits >= 32 ? 0u : (lo >> bits) << bits;
+    auto competes = [&](unsigned k) { return bits >= 32 || ((k - base) >> bits) == 0; };
+    while (bits > 0) {
+      const int shift = bits > 8 ? bits - 8 : 0;
+      for (int i = first + tid; i < tail; i += kThreads)
+        if (competes(keys[i])) atomicAdd(&hist[((keys[i] - base) >> shift) & 255], 1u);
+      __syncthreads();
+      find_bin(need);
+      const int count = (int)hist[bin_s];
+      base += (unsigned)bin_s << shift;
+      need -= above_s;
+      bits = shift;
+      __syncthreads();
+      if (bits > 0 && count <= 32) {
+        // few enough for one warp: the key with fewer than need above it and at least need from it up
+        for (int i = first + tid; i < tail; i += kThreads)
+          if (competes(keys[i])) few[atomicAdd(&few_n, 1)] = keys[i];
+        __syncthreads();
+        if (warp == 0) {
+          const unsigned k = lane < count ? few[lane] : 0u;
+          int over = 0, from = 0;
+          for (int x = 0; x < count; ++x) {
+            const unsigned o = __shfl_sync(0xffffffffu, k, x);
+            over += o > k;
+            from += o >= k;
+          }
+          if (lane < count && over < need && from >= need) thr_s = k;
+        }
+        __syncthreads();
+        base = thr_s;
+        bits = 0;
+      } else if (bits > 0) {
+        hist[tid] = 0;
+        __syncthreads();
       }
-      for (int c = tid; c < a.chunks; c += kThreads)
-        if (c * a.chunk < npg) err = fmaxf(err, __ldcg(errs + (size_t)j * a.chunks + c));
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      err = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(err)));   // err >= 0
-      if (lane == 0) {
-        wlo[warp] = lo;
-        whi[warp] = hi;
-        werr[warp] = err;
-      }
-      hist[tid] = 0;
+    }
+    // the band of 2 E around the threshold (and the rounding of its ends, and underflow)
+    const float t = score_of(base);
+    const float wide = 2.f * kErr * err + 0x1p-22f * fabsf(t) + 0x1p-100f;
+    if (wide < INFINITY) {
+      band_key = key_of(t - wide);
+      in_key = key_of(t + wide) + 1;
+    } else if (t == -INFINITY && err < INFINITY) {
+      band_key = key_of(t);           // pages without a score: they are equal
+      in_key = band_key + 1;
+    } else {
+      band_key = 0;                   // E is not finite: every page's float64 score is taken
+      in_key = ~0u;
+    }
+    int sure = 0, band = 0, n_sure, n_band;
+    for (int i = first + tid; i < tail; i += kThreads) {
+      sure += keys[i] >= in_key;
+      band += keys[i] >= band_key && keys[i] < in_key;
+    }
+    count2(sure, band, n_sure, n_band);
+    need = want - n_sure;
+    if (n_band == need) {
+      in_key = band_key;
+    } else {
+      // float64 scores of the band: the rotated query (its angles first: qr and qn give their place
+      // to it), then a warp per page
+      double* qd = reinterpret_cast<double*>(smem);
+      for (int f = tid; f < a.d_h; f += kThreads)
+        cs[f] = a.rope ? rope_double(qpos, a.omega[f < half ? f : f - half], f >= half) : f < half ? 1.0 : 0.0;
       if (tid == 0) few_n = 0;
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        lo = min(lo, wlo[w]);
-        hi = max(hi, whi[w]);
-        err = fmaxf(err, werr[w]);
+      for (int i = tid; i < a.gs * half; i += kThreads) {
+        const int h = i / half, f = i - h * half;
+        const double u = (double)Dt<DT>::to_f(q[h * a.d_h + f]), w = (double)Dt<DT>::to_f(q[h * a.d_h + half + f]);
+        qd[h * a.d_h + f] = u * cs[f] - w * cs[half + f];
+        qd[h * a.d_h + half + f] = w * cs[f] + u * cs[half + f];
       }
-      // the key of the want-th page from the top: keys in [base, base + 2^bits) still compete
-      int need = want;
-      int bits = lo == hi ? 0 : 32 - __clz((int)(lo ^ hi));
-      unsigned base = bits >= 32 ? 0u : (lo >> bits) << bits;
-      auto competes = [&](unsigned k) { return bits >= 32 || ((k - base) >> bits) == 0; };
-      while (bits > 0) {
-        const int shift = bits > 8 ? bits - 8 : 0;
+      if (n_band <= 32)
         for (int i = first + tid; i < tail; i += kThreads)
-          if (competes(keys[i])) atomicAdd(&hist[((keys[i] - base) >> shift) & 255], 1u);
-        __syncthreads();
-        find_bin(need);
-        const int count = (int)hist[bin_s];
-        base += (unsigned)bin_s << shift;
-        need -= above_s;
-        bits = shift;
-        __syncthreads();
-        if (bits > 0 && count <= 32) {
-          // few enough for one warp: the key with fewer than need above it and at least need from it up
-          for (int i = first + tid; i < tail; i += kThreads)
-            if (competes(keys[i])) few[atomicAdd(&few_n, 1)] = keys[i];
-          __syncthreads();
-          if (warp == 0) {
-            const unsigned k = lane < count ? few[lane] : 0u;
-            int over = 0, from = 0;
-            for (int x = 0; x < count; ++x) {
-              const unsigned o = __shfl_sync(0xffffffffu, k, x);
-              over += o > k;
-              from += o >= k;
-            }
-            if (lane < count && over < need && from >= need) thr_s = k;
+          if (keys[i] >= band_key && keys[i] < in_key) few[atomicAdd(&few_n, 1)] = (unsigned)i;
+      __syncthreads();
+      auto page_score = [&](int i) {     // float64 score of page i (the whole warp)
+        const int pg = a.page_table[(size_t)b * a.max_pages + i];
+        double best = -INFINITY;
+        for (int h = 0; h < a.gs && pg >= 0 && pg < a.num_pages; ++h) {
+          const T* box = bounds + ((size_t)pg * a.G + g) * 2 * a.W + h * a.d_h;
+          double s = 0.0;
+#pragma unroll 4
+          for (int c = lane; c < a.d_h; c += 32) {
+            const double x = qd[h * a.d_h + c];
+            s = fma(x, (double)Dt<DT>::to_f(x >= 0.0 ? box[a.W + c] : box[c]), s);
           }
-          __syncthreads();
-          base = thr_s;
-          bits = 0;
-        } else if (bits > 0) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+          if (s == s) best = fmax(best, s);
+        }
+        return best;
+      };
+      if (n_band <= 32) {
+        // few pages: one warp ranks them and settles their keys, kept or not
+        for (int x = warp; x < n_band; x += kWarps) {
+          const double s = page_score((int)few[x]);
+          if (lane == 0) exact_few[x] = s;
+        }
+        __syncthreads();
+        if (warp == 0) {
+          const int i = lane < n_band ? (int)few[lane] : INT32_MAX;
+          const double s = lane < n_band ? exact_few[lane] : -INFINITY;
+          int ahead = 0;
+          for (int x = 0; x < n_band; ++x) {
+            const double o = __shfl_sync(0xffffffffu, s, x);
+            const int oi = __shfl_sync(0xffffffffu, i, x);
+            ahead += o > s || (o == s && oi < i);
+          }
+          if (lane < n_band) keys[i] = ahead < need ? ~0u : 0u;
+        }
+        if (in_key == ~0u) in_key = ~0u - 1;
+        band_key = in_key;
+        __syncthreads();
+      } else {
+        for (int i = first + warp; i < tail; i += kWarps) {
+          if (!(keys[i] >= band_key && keys[i] < in_key)) continue;
+          const double s = page_score(i);
+          if (lane == 0) exact[i] = s;
+        }
+        __threadfence();
+        __syncthreads();
+        int left = 64;                                 // bits not settled yet
+        while (left > 0) {
+          const int shift = left - 8;
           hist[tid] = 0;
           __syncthreads();
-        }
-      }
-      // the band of 2 E around the threshold (and the rounding of its ends, and underflow)
-      const float t = score_of(base);
-      const float wide = 2.f * kErr * err + 0x1p-22f * fabsf(t) + 0x1p-100f;
-      if (wide < INFINITY) {
-        band_key = key_of(t - wide);
-        in_key = key_of(t + wide) + 1;
-      } else if (t == -INFINITY && err < INFINITY) {
-        band_key = key_of(t);           // pages without a score: they are equal
-        in_key = band_key + 1;
-      } else {
-        band_key = 0;                   // E is not finite: every page's float64 score is taken
-        in_key = ~0u;
-      }
-      int sure = 0, band = 0, n_sure, n_band;
-      for (int i = first + tid; i < tail; i += kThreads) {
-        sure += keys[i] >= in_key;
-        band += keys[i] >= band_key && keys[i] < in_key;
-      }
-      count2(sure, band, n_sure, n_band);
-      need = want - n_sure;
-      if (n_band == need) {
-        in_key = band_key;
-      } else {
-        // float64 scores of the band: the rotated query (its angles first: qr and qn give their place
-        // to it), then a warp per page
-        double* qd = reinterpret_cast<double*>(smem);
-        const T* q = query(j);
-        const int qp = a.q_pos[(size_t)b * a.Q + j];
-        for (int f = tid; f < a.d_h; f += kThreads)
-          cs[f] = a.rope ? rope_double(qp, a.omega[f < half ? f : f - half], f >= half) : f < half ? 1.0 : 0.0;
-        if (tid == 0) few_n = 0;
-        __syncthreads();
-        for (int i = tid; i < a.gs * half; i += kThreads) {
-          const int h = i / half, f = i - h * half;
-          const double u = (double)Dt<DT>::to_f(q[h * a.d_h + f]), w = (double)Dt<DT>::to_f(q[h * a.d_h + half + f]);
-          qd[h * a.d_h + f] = u * cs[f] - w * cs[half + f];
-          qd[h * a.d_h + half + f] = w * cs[f] + u * cs[half + f];
-        }
-        if (n_band <= 32)
           for (int i = first + tid; i < tail; i += kThreads)
-            if (keys[i] >= band_key && keys[i] < in_key) few[atomicAdd(&few_n, 1)] = (unsigned)i;
-        __syncthreads();
-        auto page_score = [&](int i) {     // float64 score of page i (the whole warp)
-          const int pg = a.page_table[(size_t)b * a.max_pages + i];
-          double best = -INFINITY;
-          for (int h = 0; h < a.gs && pg >= 0 && pg < a.num_pages; ++h) {
-            const T* box = bounds + ((size_t)pg * a.G + g) * 2 * a.W + h * a.d_h;
-            double s = 0.0;
-#pragma unroll 4
-            for (int c = lane; c < a.d_h; c += 32) {
-              const double x = qd[h * a.d_h + c];
-              s = fma(x, (double)Dt<DT>::to_f(x >= 0.0 ? box[a.W + c] : box[c]), s);
+            if (keys[i] >= band_key && keys[i] < in_key) {
+              const unsigned long long k = key_of(__ldcg(exact + i));
+              if (left == 64 || (k >> left) == (thr >> left)) atomicAdd(&hist[(k >> shift) & 255], 1u);
             }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            if (s == s) best = fmax(best, s);
-          }
-          return best;
-        };
-        if (n_band <= 32) {
-          // few pages: one warp ranks them and settles their keys, kept or not
-          for (int x = warp; x < n_band; x += kWarps) {
-            const double s = page_score((int)few[x]);
-            if (lane == 0) exact_few[x] = s;
-          }
           __syncthreads();
-          if (warp == 0) {
-            const int i = lane < n_band ? (int)few[lane] : INT32_MAX;
-            const double s = lane < n_band ? exact_few[lane] : -INFINITY;
-            int ahead = 0;
-            for (int x = 0; x < n_band; ++x) {
-              const double o = __shfl_sync(0xffffffffu, s, x);
-              const int oi = __shfl_sync(0xffffffffu, i, x);
-              ahead += o > s || (o == s && oi < i);
-            }
-            if (lane < n_band) keys[i] = ahead < need ? ~0u : 0u;
-          }
-          if (in_key == ~0u) in_key = ~0u - 1;
-          band_key = in_key;
+          find_bin(need);
+          thr |= (unsigned long long)bin_s << shift;
+          need -= above_s;
+          left = shift;
           __syncthreads();
-        } else {
-          for (int i = first + warp; i < tail; i += kWarps) {
-            if (!(keys[i] >= band_key && keys[i] < in_key)) continue;
-            const double s = page_score(i);
-            if (lane == 0) exact[i] = s;
-          }
-          __threadfence();
-          __syncthreads();
-          int left = 64;                                 // bits not settled yet
-          while (left > 0) {
-            const int shift = left - 8;
-            hist[tid] = 0;
-            __syncthreads();
-            for (int i = first + tid; i < tail; i += kThreads)
-              if (keys[i] >= band_key && keys[i] < in_key) {
-                const unsigned long long k = key_of(__ldcg(exact + i));
-                if (left == 64 || (k >> left) == (thr >> left)) atomicAdd(&hist[(k >> shift) & 255], 1u);
-              }
-            __syncthreads();
-            find_bin(need);
-            thr |= (unsigned long long)bin_s << shift;
-            need -= above_s;
-            left = shift;
-            __syncthreads();
-          }
-          ties = need;
         }
+        ties = need;
       }
     }
-    // compaction in index order
-    const bool exact_band = ties > 0;
-    int32_t* list = a.list + li * a.K;
-    float* so = a.scores_out != nullptr ? a.scores_out + li * a.K : nullptr;
-    int done = 0, tied = 0;
-    for (int i0 = 0; i0 < seen; i0 += kThreads) {
-      const int i = i0 + tid;
-      const bool mid = i >= first && i < tail;
-      bool keep = i < seen && !mid, in_band = false, tie = false;
-      if (mid && in_key != ~0u) {
-        const unsigned k = in_key != 0 ? keys[i] : ~0u;
-        keep = k >= in_key;
-        in_band = exact_band && !keep && k >= band_key;
-      } else if (mid && exact_band) {
-        in_band = keys[i] >= band_key;
-      }
-      if (in_band) {
-        const unsigned long long k = key_of(__ldcg(exact + i));
-        keep = k > thr;
-        tie = k == thr;
-      }
-      if (exact_band) {
-        const unsigned tb = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) wband[warp] = __popc(tb);
-        __syncthreads();
-        int t = tied + __popc(tb & below);
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < warp) t += wband[w];
-          tied += wband[w];
-        }
-        if (tie && t < ties) keep = true;
-        __syncthreads();
-      }
-      const unsigned kb = __ballot_sync(0xffffffffu, keep);
-      if (lane == 0) wcount[warp] = __popc(kb);
+  }
+  // compaction in index order
+  const bool exact_band = ties > 0;
+  int32_t* list = a.list + li * a.K;
+  float* so = a.scores_out != nullptr ? a.scores_out + li * a.K : nullptr;
+  int done = 0, tied = 0;
+  for (int i0 = 0; i0 < seen; i0 += kThreads) {
+    const int i = i0 + tid;
+    const bool mid = i >= first && i < tail;
+    bool keep = i < seen && !mid, in_band = false, tie = false;
+    if (mid && in_key != ~0u) {
+      const unsigned k = in_key != 0 ? keys[i] : ~0u;
+      keep = k >= in_key;
+      in_band = exact_band && !keep && k >= band_key;
+    } else if (mid && exact_band) {
+      in_band = keys[i] >= band_key;
+    }
+    if (in_band) {
+      const unsigned long long k = key_of(__ldcg(exact + i));
+      keep = k > thr;
+      tie = k == thr;
+    }
+    if (exact_band) {
+      const unsigned tb = __ballot_sync(0xffffffffu, tie);
+      if (lane == 0) wband[warp] = __popc(tb);
       __syncthreads();
-      int at = done + __popc(kb & below);
+      int t = tied + __popc(tb & below);
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) at += wcount[w];
-        done += wcount[w];
+        if (w < warp) t += wband[w];
+        tied += wband[w];
       }
-      if (keep && at < a.K) {
-        list[at] = i;
-        if (so != nullptr)
-          so[at] = in_band ? (float)__ldcg(exact + i) : __ldcg(sc + i);
-      }
+      if (tie && t < ties) keep = true;
       __syncthreads();
     }
-    for (int i = m + tid; i < a.K; i += kThreads) {
-      list[i] = -1;
-      if (so != nullptr) so[i] = -INFINITY;
+    const unsigned kb = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) wcount[warp] = __popc(kb);
+    __syncthreads();
+    int at = done + __popc(kb & below);
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += wcount[w];
+      done += wcount[w];
     }
-    if (tid == 0) a.counts[li] = m;
+    if (keep && at < a.K) {
+      list[at] = i;
+      if (so != nullptr)
+        so[at] = in_band ? (float)__ldcg(exact + i) : __ldcg(sc + i);
+    }
     __syncthreads();
   }
+  for (int i = m + tid; i < a.K; i += kThreads) {
+    list[i] = -1;
+    if (so != nullptr) so[i] = -INFINITY;
+  }
+  if (tid == 0) a.counts[li] = m;
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -688,7 +676,7 @@ int chunk_of(long long lists, int max_pages) {
 
 template <int DT>
 cudaError_t launch(SelectArgs a, cudaStream_t st) {
-  const dim3 grid(a.chunks, a.G, a.batch);
+  const dim3 grid(a.chunks, a.G * a.Q, a.batch);
   const int lanes_h = a.d_h / kVec;   // lanes a head takes in the vector form
   const size_t slots = (size_t)2 * a.W * Dt<DT>::bytes * kWarps * kSlots;
   const bool vec =
@@ -733,7 +721,7 @@ cudaError_t launch_select(const palu_config* c, int batch, int num_queries, cons
   a.n_first = num_first;
   a.n_last = num_last;
   a.K = list_len;
-  a.chunk = chunk_of((long long)batch * a.G, max_pages);
+  a.chunk = chunk_of((long long)batch * a.G * num_queries, max_pages);
   a.chunks = (max_pages + a.chunk - 1) / a.chunk;
   a.rope = c->rope_base != 0.f;
   a.causal = num_queries > 1 && !explicit_pos;

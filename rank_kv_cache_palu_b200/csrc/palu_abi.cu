@@ -831,7 +831,7 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
       num_last < 0 || list_len <= 0 || (long long)num_first + num_last > list_len)
     return PALU_ERR_INVALID_ARG;
   const long long G = cfg->num_heads / cfg->group_size;
-  if (batch * G > PALU_SELECT_MAX_LISTS || batch > 65535 || max_pages > PALU_SELECT_MAX_PAGES ||
+  if (batch * G * num_queries > PALU_SELECT_MAX_LISTS || batch > 65535 || max_pages > PALU_SELECT_MAX_PAGES ||
       (long long)cfg->group_size * cfg->head_dim > 8192)
     return PALU_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < palu::select_workspace(cfg, batch, num_queries, max_pages))

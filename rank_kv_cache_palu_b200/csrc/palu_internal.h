@@ -122,6 +122,8 @@ TimeoutTest timeout_test_setting();
 
 // CUDA-core kernels (any supported dtype; the only path for float32).
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t st);
+// The CUDA-core split kernel over page lists (DecodeArgs::page_list set); launch_decode_simt calls it.
+cudaError_t launch_decode_pages_simt(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t st);
 // The merge after a walk over page lists (DecodeArgs::segments set); launch_combine calls it.
 cudaError_t launch_pages_combine(const DecodeArgs& a, cudaStream_t st);
