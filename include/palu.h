@@ -323,7 +323,8 @@ palu_status palu_decode_attn_noalloc(const palu_config* cfg, int batch, const vo
  *   taken      [batch] int32 or NULL (written): num_new[b], or 0 where refused
  * Pages come off the top of the stack in (sequence, page) order.  A sequence
  * gets all the pages it needs or none: it is refused (its length and table stay)
- * when the needs of the sequences up to it exceed num_free.  Pages given back
+ * when the needs of the sequences up to it exceed num_free.  A page belongs to
+ * one sequence (one that two share would be given back twice).  Pages given back
  * go on top of what is left, the last in (sequence, page) order first, so
  * dropping what the last call appended restores the stack; they serve the next
  * call, not this one.
@@ -390,7 +391,8 @@ palu_status palu_page_bounds_bytes(const palu_config* cfg, size_t* bytes_per_pag
  * every sequence (first NULL: all of its pages), each from all its cached
  * tokens: after an append, first[b] is the first appended token; after dropping
  * tokens, the sequence's new length (its last page shrank).  Pages past the
- * sequence and pages before first[b] stay as they are.
+ * sequence and pages before first[b] stay as they are.  A page that two sequences
+ * hold must be as full in both.
  *   first [batch] int32 or NULL; ranks_k [G] HOST int32 or NULL (per-group key
  *   ranks, as in the ranked calls); the rest as in palu_decode_attn. */
 palu_status palu_page_bounds_workspace_size(const palu_config* cfg, int batch, int max_pages, size_t* bytes);
@@ -436,6 +438,9 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
  * page_list[b][j][g][0 .. page_counts[b][j][g]) instead of all.
  *   page_list   [batch][num_queries][G][list_len] int32, strictly ascending
  *   page_counts [batch][num_queries][G] int32 in [0, list_len]; 0: out = 0, lse = -inf
+ * Cached latents of tokens that a query does not see may be anything (NaN too);
+ * with num_queries > 1 and a position pool those of the sequence's own tokens must
+ * be finite on the tensor-core kernels.
  * A list that is not ascending or names a page past the sequence is reported as
  * PALU_ERR_DEVICE_BOUNDS (the result is void).  The softmax weights reach the
  * value product as the sum of two 16-bit numbers, so F16 / BF16 results carry

@@ -453,7 +453,7 @@ def palu_page_bounds(cfg: PaluConfig, first, zk_pool, zk_scales, pos_pool, page_
     batch, max_pages = page_table.shape
     if bounds.numel() < _bounds_numel(cfg, num_pages):
         raise ValueError(f"palu_page_bounds: bounds holds fewer than {num_pages} pages")
-    rk = ranks_k or (cfg.rank_k,) * (cfg.num_heads // cfg.group_size)
+    rk = (cfg.rank_k,) * (cfg.num_heads // cfg.group_size) if ranks_k is None else ranks_k
     kb, ksb = _page_bytes(cfg, rk)
     A.call(load().palu_page_bounds, ctypes.byref(cfg), _ranks(ranks_k), batch, A("first", first, _I32, (batch,)),
            _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
@@ -512,7 +512,7 @@ def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scale
     batch, Q = q_pos.shape
     G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
     rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _ACT_TORCH.get(cfg.act_dtype)
-    rk, rv = ranks_k or (cfg.rank_k,) * G, ranks_v or (cfg.rank_v,) * G
+    rk, rv = ((cfg.rank_k,) * G, (cfg.rank_v,) * G) if ranks_k is None else (ranks_k, ranks_v)
     (kb, ksb), (vb, vsb) = _page_bytes(cfg, rk), _page_bytes(cfg, rv)
     query, at, table, lens, lists, counts, result = A.take(
         _ATTEND, (q, q_pos, page_table, seq_lens, page_list, page_counts, out), [act, _I32, _I32, _I32, _I32, _I32, act],

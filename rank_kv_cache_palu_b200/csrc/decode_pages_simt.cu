@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(kThreads) decode_pages_simt_kernel(const __gri
     const uint8_t* zv = a.gm.zv[gi] + (size_t)page * a.gm.v_page;
     const uint8_t* zks = LAT == PALU_INT4 ? a.gm.zks[gi] + (size_t)page * a.gm.ks_page : nullptr;
     const uint8_t* zvs = LAT == PALU_INT4 ? a.gm.zvs[gi] + (size_t)page * a.gm.vs_page : nullptr;
-    const int rows = min(a.P, lr.T - lp * a.P);
+    // a query of several sees the tokens up to its own (a position may be any where they are explicit)
+    const int seen = a.causal && a.pos_pool == nullptr ? min(lr.T, max(0, min(qpos, lr.T) + 1)) : lr.T;
+    const int rows = min(a.P, max(0, seen - lp * a.P));
     auto position = [&](int t) {
       return a.pos_pool != nullptr ? a.pos_pool[(size_t)page * a.P + t] : lp * a.P + t;
     };
@@ -175,11 +177,11 @@ __global__ void __launch_bounds__(kThreads) decode_pages_simt_kernel(const __gri
           if (r >= a.r_v) continue;
           float v = acc[k] * resc;
 #pragma unroll 8
-          for (int t = vg; t < nt; t += vgroups)
-            v = fmaf(ps[t],
-                     load_latent<LAT, ACT>(zv, t0 + t, a.P,
-                                           LAT == PALU_INT4 ? zvs + (size_t)(t0 + t) * a.vs_row : nullptr, r),
-                     v);
+          for (int t = vg; t < nt; t += vgroups) {
+            const float z = load_latent<LAT, ACT>(
+                zv, t0 + t, a.P, LAT == PALU_INT4 ? zvs + (size_t)(t0 + t) * a.vs_row : nullptr, r);
+            v = ps[t] != 0.f ? fmaf(ps[t], z, v) : v;      // a masked token's latents may be anything
+          }
           acc[k] = v;
         }
       }

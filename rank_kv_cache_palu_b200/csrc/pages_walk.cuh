@@ -23,7 +23,7 @@ struct Tile {
   int page;    // physical page; -1: outside the pool (reported, its data are another page's)
   int lp;      // logical page
   int unit;    // query
-  int info;    // valid rows (0..128) and the flags below
+  int info;    // rows the query sees (0..128) and the flags below
 };
 constexpr int kTileRows = 255, kTileFirst = 256, kTileLast = 512, kTileCont = 1024;
 __device__ __forceinline__ int tile_rows(int info) { return info & kTileRows; }
@@ -97,7 +97,10 @@ __device__ __forceinline__ int walk_tiles(const DecodeArgs& a, int g, int gi, bo
       report(st, PALU_ERR_DEVICE_BOUNDS, 3000000 + u);   // not ascending, or past the sequence
       t.lp = 0;
     } else {
-      rows = min(a.P, T - lp * a.P);
+      // a query of several sees the tokens up to its own: where positions are the tokens' places the
+      // later ones are rows past the end to it, so nothing of them reaches the value product
+      const int seen = a.causal && a.pos_pool == nullptr ? min(T, max(0, min(a.q_pos[u], T) + 1)) : T;
+      rows = min(a.P, max(0, seen - lp * a.P));
       t.page = a.page_table[(size_t)sb * a.max_pages + lp];
       if (t.page < 0 || t.page >= a.num_pages) {
         report(st, PALU_ERR_DEVICE_BOUNDS, 2000000 + sb);

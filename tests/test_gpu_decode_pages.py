@@ -226,6 +226,25 @@ def test_rows_behind_the_last_token_are_not_read(name):
     compare(case, *run(case, pools, q, q_pos, lists, 2), q, q_pos, lists, uniform(case))
 
 
+@pytest.mark.parametrize("name", ["bf16", "norope", "tiny_f32"])
+def test_tokens_after_the_query_may_hold_anything(name):
+    """NaN and infinities in the latents of the drafts behind a query do not reach its result."""
+    case = make_decode_case(CASES[name][0], [260])
+    w = case.w
+    q, _ = queries(case, 3)
+    q_pos = np.array([[126, 255, 256]], np.int32)            # the last token of a page but one, the last, the first
+    pools = build_pools(case)
+    T = TORCH_DTYPE[w.latent_dtype]
+    lists = [[[[0, 1]] * w.groups, [[1]] * w.groups, [[0, 2]] * w.groups]]
+    for t in range(257, 260):
+        for pool, rank in (("zk", w.rank_k), ("zv", w.rank_v)):
+            raw = pools[pool].view(case.num_pages, w.groups, rank * T.itemsize // 128, w.page_size, 128)
+            junk = raw[int(case.page_table[0, t // w.page_size]), :, :, t % w.page_size].contiguous().view(T)
+            junk[..., 0::2], junk[..., 1::2] = float("nan"), float("inf")
+            raw[int(case.page_table[0, t // w.page_size]), :, :, t % w.page_size] = junk.view(torch.uint8)
+    compare(case, *run(case, pools, q, q_pos, lists, 2), q, q_pos, lists, uniform(case))
+
+
 @pytest.mark.parametrize("name", ["bf16", "int4_f16", "norope"])
 def test_timeout_reports_and_recovers(name):
     case = make_decode_case(CASES[name][0], [600])
