@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -410,17 +411,21 @@ _VERIFY = ("draft_tokens", "u_accept", "u_sample", "tokens", "num_accepted")
 _ACT_TORCH = {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
 
 
-def _bounds_numel(cfg: PaluConfig, num_pages: int) -> int:
-    return num_pages * 2 * cfg.num_heads * cfg.head_dim
+class _Layer(NamedTuple):
+    """What the checks of these calls take from a config and its ranks."""
 
-
-def palu_page_bounds_bytes(cfg: PaluConfig) -> int:
-    """Bytes of one page of the bounds pool [num_pages][G][2][group width], act dtype."""
-    return _size("palu_page_bounds_bytes", ctypes.byref(cfg))
-
-
-def palu_page_bounds_workspace_size(cfg: PaluConfig, batch: int, max_pages: int) -> int:
-    return _size("palu_page_bounds_workspace_size", ctypes.byref(cfg), batch, max_pages)
+    act: torch.dtype
+    groups: int
+    heads: int
+    head_dim: int
+    bounds: int          # entries of a page's bounds
+    rows_k: int          # entries of B_k, B_v
+    rows_v: int
+    zk: int              # bytes per page of each pool
+    zv: int
+    zks: int
+    zvs: int
+    pos: int
 
 
 def _page_bytes(cfg: PaluConfig, ranks) -> tuple[int, int]:
@@ -430,11 +435,23 @@ def _page_bytes(cfg: PaluConfig, ranks) -> tuple[int, int]:
     return cfg.page_size * sum(ranks) // 2, cfg.page_size * sum((r // 32 * 2 + 15) // 16 * 16 for r in ranks)
 
 
-def _factor(A, name, B, cfg, ranks):
-    """B_k or B_v: the groups' [rank][group width] blocks, back to back."""
-    if B.numel() != sum(ranks) * cfg.group_size * cfg.head_dim:
-        raise ValueError(f"{A.where}: {name} must hold {sum(ranks)} rows of {cfg.group_size * cfg.head_dim}")
-    return A(name, B, _ACT_TORCH.get(cfg.act_dtype))
+_uniform: dict[bytes, _Layer] = {}       # by the config's bytes: constants of a config, not of a call
+
+
+def _layer(cfg: PaluConfig, ranks_k=None, ranks_v=None) -> _Layer:
+    if ranks_k is None:
+        found = _uniform.get(bytes(cfg))
+        if found is not None:
+            return found
+    G = cfg.num_heads // cfg.group_size
+    rk, rv = ((cfg.rank_k,) * G, (cfg.rank_v,) * G) if ranks_k is None else (ranks_k, ranks_v)
+    (zk, zks), (zv, zvs) = _page_bytes(cfg, rk), _page_bytes(cfg, rv)
+    width = cfg.group_size * cfg.head_dim
+    made = _Layer(_ACT_TORCH.get(cfg.act_dtype), G, cfg.num_heads, cfg.head_dim, 2 * G * width, sum(rk) * width,
+                  sum(rv) * width, zk, zv, zks, zvs, 4 * cfg.page_size)
+    if ranks_k is None and len(_uniform) < 256:
+        _uniform[bytes(cfg)] = made
+    return made
 
 
 def _pool(A, name, pool, num_pages, page_bytes):
@@ -446,21 +463,39 @@ def _pool(A, name, pool, num_pages, page_bytes):
     return A(name, pool, None)
 
 
+def _sized(A, name, t, dtype, entries):
+    """A tensor of exactly `entries` entries, whatever its shape."""
+    if t.numel() != entries:
+        raise ValueError(f"{A.where}: {name} must hold {entries} entries, got {t.numel()}")
+    return A(name, t, dtype)
+
+
+def _bounds(A, bounds, dtype, entries):
+    if bounds.numel() < entries:
+        raise ValueError(f"{A.where}: bounds holds fewer pages than the cache")
+    return A("bounds", bounds, dtype)
+
+
+def palu_page_bounds_bytes(cfg: PaluConfig) -> int:
+    """Bytes of one page of the bounds pool [num_pages][G][2][group width], act dtype."""
+    return _size("palu_page_bounds_bytes", ctypes.byref(cfg))
+
+
+def palu_page_bounds_workspace_size(cfg: PaluConfig, batch: int, max_pages: int) -> int:
+    return _size("palu_page_bounds_workspace_size", ctypes.byref(cfg), batch, max_pages)
+
+
 def palu_page_bounds(cfg: PaluConfig, first, zk_pool, zk_scales, pos_pool, page_table, seq_lens, num_pages: int, B_k,
                      bounds, workspace, ranks_k=None, stream=None):
     """Rebuild the key bounds of the pages holding tokens first[b] .. seq_lens[b] - 1 (first None: all)."""
-    A = _Args("palu_page_bounds", workspace)
+    A, L = _Args("palu_page_bounds", workspace), _layer(cfg, ranks_k, ranks_k)
     batch, max_pages = page_table.shape
-    if bounds.numel() < _bounds_numel(cfg, num_pages):
-        raise ValueError(f"palu_page_bounds: bounds holds fewer than {num_pages} pages")
-    rk = (cfg.rank_k,) * (cfg.num_heads // cfg.group_size) if ranks_k is None else ranks_k
-    kb, ksb = _page_bytes(cfg, rk)
+    table, lens = A.take(("page_table", "seq_lens"), (page_table, seq_lens), [_I32, _I32], [(batch, max_pages), (batch,)])
     A.call(load().palu_page_bounds, ctypes.byref(cfg), _ranks(ranks_k), batch, A("first", first, _I32, (batch,)),
-           _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zk_scales", zk_scales, num_pages, ksb),
-           _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size), A("page_table", page_table, _I32), max_pages,
-           A("seq_lens", seq_lens, _I32, (batch,)), num_pages, _factor(A, "B_k", B_k, cfg, rk),
-           A("bounds", bounds, _ACT_TORCH.get(cfg.act_dtype)), A("workspace", workspace, None),
-           workspace.nbytes, stream=stream)
+           _pool(A, "zk_pool", zk_pool, num_pages, L.zk), _pool(A, "zk_scales", zk_scales, num_pages, L.zks),
+           _pool(A, "pos_pool", pos_pool, num_pages, L.pos), table, max_pages, lens, num_pages,
+           _sized(A, "B_k", B_k, L.act, L.rows_k), _bounds(A, bounds, L.act, num_pages * L.bounds),
+           A("workspace", workspace, None), workspace.nbytes, stream=stream)
 
 
 def palu_select_workspace_size(cfg: PaluConfig, batch: int, num_queries: int, max_pages: int) -> int:
@@ -474,18 +509,14 @@ def palu_select_pages(cfg: PaluConfig, q, q_pos, bounds, pos_pool, page_table, s
     q [batch][Q][H][d_h], q_pos [batch][Q]; page_list [batch][Q][G][list_len] (ascending, then -1),
     page_counts [batch][Q][G] and page_scores (like page_list, or None) are written.
     """
-    A = _Args("palu_select_pages", workspace)
+    A, L = _Args("palu_select_pages", workspace), _layer(cfg)
     batch, Q = q_pos.shape
-    G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
-    if bounds.numel() < _bounds_numel(cfg, num_pages):
-        raise ValueError(f"palu_select_pages: bounds holds fewer than {num_pages} pages")
+    G, max_pages, keep = L.groups, page_table.shape[1], page_list.shape[-1]
     query, at, table, lens, lists, counts = A.take(
-        _SELECT, (q, q_pos, page_table, seq_lens, page_list, page_counts),
-        [_ACT_TORCH.get(cfg.act_dtype), _I32, _I32, _I32, _I32, _I32],
-        [(batch, Q, cfg.num_heads, cfg.head_dim), (batch, Q), (batch, max_pages), (batch,), (batch, Q, G, keep),
-         (batch, Q, G)])
+        _SELECT, (q, q_pos, page_table, seq_lens, page_list, page_counts), [L.act, _I32, _I32, _I32, _I32, _I32],
+        [(batch, Q, L.heads, L.head_dim), (batch, Q), (batch, max_pages), (batch,), (batch, Q, G, keep), (batch, Q, G)])
     A.call(load().palu_select_pages, ctypes.byref(cfg), batch, Q, query, at,
-           A("bounds", bounds, _ACT_TORCH.get(cfg.act_dtype)), A("pos_pool", pos_pool, _I32), table, max_pages, lens,
+           _bounds(A, bounds, L.act, num_pages * L.bounds), A("pos_pool", pos_pool, _I32), table, max_pages, lens,
            num_pages, num_first, num_last, keep, lists, counts,
            A("page_scores", page_scores, _F32, (batch, Q, G, keep)), A("workspace", workspace, None),
            workspace.nbytes, stream=stream)
@@ -508,22 +539,19 @@ def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scale
 
     q and out [batch][Q][H][d_h], q_pos [batch][Q], lse [batch][Q][H] or None; Q > 1 is causal by position.
     """
-    A = _Args("palu_decode_attn_pages", workspace)
+    A, L = _Args("palu_decode_attn_pages", workspace), _layer(cfg, ranks_k, ranks_v)
     batch, Q = q_pos.shape
-    G, max_pages, keep = cfg.num_heads // cfg.group_size, page_table.shape[1], page_list.shape[-1]
-    rows, act = (batch, Q, cfg.num_heads, cfg.head_dim), _ACT_TORCH.get(cfg.act_dtype)
-    rk, rv = ((cfg.rank_k,) * G, (cfg.rank_v,) * G) if ranks_k is None else (ranks_k, ranks_v)
-    (kb, ksb), (vb, vsb) = _page_bytes(cfg, rk), _page_bytes(cfg, rv)
+    G, max_pages, keep, rows = L.groups, page_table.shape[1], page_list.shape[-1], (batch, Q, L.heads, L.head_dim)
     query, at, table, lens, lists, counts, result = A.take(
-        _ATTEND, (q, q_pos, page_table, seq_lens, page_list, page_counts, out), [act, _I32, _I32, _I32, _I32, _I32, act],
+        _ATTEND, (q, q_pos, page_table, seq_lens, page_list, page_counts, out),
+        [L.act, _I32, _I32, _I32, _I32, _I32, L.act],
         [rows, (batch, Q), (batch, max_pages), (batch,), (batch, Q, G, keep), (batch, Q, G), rows])
     A.call(load().palu_decode_attn_pages, ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch, Q, query, at,
-           _pool(A, "zk_pool", zk_pool, num_pages, kb), _pool(A, "zv_pool", zv_pool, num_pages, vb),
-           _pool(A, "zk_scales", zk_scales, num_pages, ksb), _pool(A, "zv_scales", zv_scales, num_pages, vsb),
-           _pool(A, "pos_pool", pos_pool, num_pages, 4 * cfg.page_size), table, max_pages, lens, lists, counts, keep,
-           num_pages, _factor(A, "B_k", B_k, cfg, rk), _factor(A, "B_v", B_v, cfg, rv), result,
-           A("lse", lse, _F32, rows[:3]), A("workspace", workspace, None),
-           workspace.nbytes, num_splits, stream=stream)
+           _pool(A, "zk_pool", zk_pool, num_pages, L.zk), _pool(A, "zv_pool", zv_pool, num_pages, L.zv),
+           _pool(A, "zk_scales", zk_scales, num_pages, L.zks), _pool(A, "zv_scales", zv_scales, num_pages, L.zvs),
+           _pool(A, "pos_pool", pos_pool, num_pages, L.pos), table, max_pages, lens, lists, counts, keep, num_pages,
+           _sized(A, "B_k", B_k, L.act, L.rows_k), _sized(A, "B_v", B_v, L.act, L.rows_v), result,
+           A("lse", lse, _F32, rows[:3]), A("workspace", workspace, None), workspace.nbytes, num_splits, stream=stream)
 
 
 _ATTEND = ("q", "q_pos", "page_table", "seq_lens", "page_list", "page_counts", "out")
