@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
             e += __shfl_xor_sync(0xffffffffu, e, off);
           }
           if (s == s) best = fmaxf(best, s);
-          if (e == e) err = e < INFINITY ? fmaxf(err, e) : INFINITY;
+          if (s == s || e == e) err = e < INFINITY ? fmaxf(err, e) : INFINITY;   // (both NaN: a NaN entry)
         }
         if (lane == 0) mine[k * kWarps] = best;
       }

@@ -191,3 +191,23 @@ def test_tiny_and_huge_scores():
         c = make(w, [PAGE * 200], seed=8)
         c["bounds"] *= scale
         check(c, 31, scores=False)
+
+
+@pytest.mark.parametrize("name", ["tiny_f32", "d20_f32"])
+def test_an_error_bound_that_overflows(name):
+    """|q_c| + |q_pair(c)| past float32's range where the bounds are zero: the float32 sums stay finite
+    but nothing is known of their error, and here one of them is wrong."""
+    w = dataclasses.replace(SHAPES[name], rope_base=0.0, num_heads=2, group_size=1)
+    c = make(w, [2 * PAGE])
+    d = w.head_dim
+    c["q"].fill_(1.0)
+    c["q"][..., 3] = c["q"][..., 3 + d // 2] = 3e38
+    c["bounds"].zero_()
+    first, second = (c["bounds"][int(c["table"][0, i])] for i in (0, 1))
+    first[..., 1] = 0.5
+    for i, v in ((0, 2.0 ** 25), (1, 1.0), (4, -2.0 ** 25)):     # 1 in exact arithmetic, 0 in float32
+        second[..., i] = v
+    check(c, 1, 0, 0, scores=False)
+    second[..., 1] = 0.0
+    second[..., 8] = 1.0
+    check(c, 1, 0, 0, scores=False)
