@@ -300,8 +300,12 @@ palu_status palu_decode_attn_noalloc(const palu_config* cfg, int batch, const vo
  * Workspaces of these calls hold counters: zero-fill a workspace once before
  * its first use and keep it to one of the calls (of any sizes it is large enough
  * for); every call leaves its counters back at zero.  Calls that overlap on the
- * GPU need workspaces of their own.  The current device must be
- * the one that owns `stream` and the pointers. */
+ * GPU need workspaces of their own.  Arrays that a call writes overlap no other
+ * array of the call.  max_pages·page_size is below 2^31 (PALU_ERR_UNSUPPORTED
+ * otherwise).  The current device must be the one that owns `stream` and the
+ * pointers; pointers that are not aligned to their elements (16 bytes for queries,
+ * pools, weights and outputs of 16-bit or float type) are refused
+ * (PALU_ERR_ALIGNMENT). */
 
 /* Append plan: pages, slots and positions of the tokens a step appends.
  *   num_new    [batch] int32        tokens sequence b appends; negative: it drops
@@ -448,7 +452,7 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
  * the lists of the CUDA-core kernel; the tensor-core kernels deal all listed pages
  * of a head group out in equal shares and take any value.  ranks_k / ranks_v as in
  * the ranked calls.
- * batch·num_queries <= 65535 (PALU_ERR_UNSUPPORTED above). */
+ * batch·num_queries <= 65535, list_len <= 2^24 (PALU_ERR_UNSUPPORTED above). */
 palu_status palu_decode_pages_workspace_size(const palu_config* cfg, const int32_t* ranks_k,
                                              const int32_t* ranks_v, int batch, int num_queries, int list_len,
                                              int num_splits, size_t* bytes);

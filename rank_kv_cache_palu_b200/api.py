@@ -439,12 +439,16 @@ _uniform: dict[bytes, _Layer] = {}       # by the config's bytes: constants of a
 
 
 def _layer(cfg: PaluConfig, ranks_k=None, ranks_v=None) -> _Layer:
+    if (ranks_k is None) != (ranks_v is None):
+        raise ValueError("ranks_k and ranks_v must be given together")
     if ranks_k is None:
         found = _uniform.get(bytes(cfg))
         if found is not None:
             return found
-    G = cfg.num_heads // cfg.group_size
+    G = cfg.num_heads // max(1, cfg.group_size)
     rk, rv = ((cfg.rank_k,) * G, (cfg.rank_v,) * G) if ranks_k is None else (ranks_k, ranks_v)
+    if len(rk) != G or len(rv) != G:
+        raise ValueError(f"ranks of {G} head groups expected, got {len(rk)} and {len(rv)}")
     (zk, zks), (zv, zvs) = _page_bytes(cfg, rk), _page_bytes(cfg, rv)
     width = cfg.group_size * cfg.head_dim
     made = _Layer(_ACT_TORCH.get(cfg.act_dtype), G, cfg.num_heads, cfg.head_dim, 2 * G * width, sum(rk) * width,
@@ -527,6 +531,7 @@ _SELECT = ("q", "q_pos", "page_table", "seq_lens", "page_list", "page_counts")
 
 def palu_decode_pages_workspace_size(cfg: PaluConfig, batch: int, num_queries: int, list_len: int,
                                      num_splits: int = 0, ranks_k=None, ranks_v=None) -> int:
+    _layer(cfg, ranks_k, ranks_v)        # checks the number of ranks
     return _size("palu_decode_pages_workspace_size", ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch,
                  num_queries, list_len, num_splits)
 

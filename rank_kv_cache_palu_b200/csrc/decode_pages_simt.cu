@@ -22,7 +22,6 @@ namespace {
 struct ListRange {
   const int32_t* list;   // entry e0 of the list
   int n, T, npg, sb;     // entries, cached tokens, pages and index of the sequence
-  bool ragged_last;      // the last entry is the sequence's partial last page
 };
 
 // This CTA's share (split blockIdx.x of a.S) of the list of virtual sequence vb
@@ -54,7 +53,6 @@ __device__ __forceinline__ ListRange list_range(const DecodeArgs& a, int vb, int
   }
   r.list = list + e0;
   r.n = e1 - e0;
-  r.ragged_last = r.n > 0 && T % a.P != 0 && r.list[r.n - 1] >= r.npg - 1;
   return r;
 }
 

@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "palu_common.cuh"
 #include "palu_internal.h"
@@ -31,6 +32,14 @@ namespace {
 using palu::cuda_status;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(std::initializer_list<const void*> all) {
+  for (const void* p : all)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
+  return true;
+}
+// Kernels count a sequence's tokens and a column's listed pages in 32 bits.
+bool countable(const palu_config* c, int max_pages) { return (long long)max_pages * c->page_size <= INT32_MAX; }
+constexpr int kMaxList = 1 << 24;
 
 palu_status check_config(const palu_config* c) {
   if (c == nullptr) return PALU_ERR_INVALID_ARG;
@@ -496,7 +505,8 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
     return PALU_ERR_INVALID_ARG;
   const int walk = sparse ? sparse->len : max_pages;   // pages a query can walk
   if (num_splits > walk) return PALU_ERR_INVALID_ARG;
-  if (sparse && (long long)batch * Q > 65535) return PALU_ERR_UNSUPPORTED;
+  if (sparse && ((long long)batch * Q > 65535 || walk > kMaxList || !countable(cfg, max_pages)))
+    return PALU_ERR_UNSUPPORTED;
   size_t fused_off = 0;
   const size_t need = sparse ? pages_workspace(L, batch, Q, walk, num_splits)
                              : decode_workspace(L, batch, Q, max_pages, num_splits, &fused_off);
@@ -510,6 +520,9 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
   if (int4 && (!zk_scales || !zv_scales)) return PALU_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(zk_pool) || !aligned16(zv_pool) || !aligned16(B_k) ||
       !aligned16(B_v) || (int4 && (!aligned16(zk_scales) || !aligned16(zv_scales))))
+    return PALU_ERR_ALIGNMENT;
+  if (sparse && (!aligned16(out) ||
+                 !aligned4({q_pos, pos_pool, page_table, seq_lens, sparse->list, sparse->counts, lse})))
     return PALU_ERR_ALIGNMENT;
 
   palu::DecodeArgs a{};
@@ -740,7 +753,7 @@ palu_status palu_decode_pages_workspace_size(const palu_config* cfg, const int32
   if (bytes == nullptr || batch < 0 || list_len <= 0 || num_splits < 0 || num_splits > list_len || num_queries < 1 ||
       num_queries > kMaxQueries)
     return PALU_ERR_INVALID_ARG;
-  if ((long long)batch * num_queries > 65535) return PALU_ERR_UNSUPPORTED;
+  if ((long long)batch * num_queries > 65535 || list_len > kMaxList) return PALU_ERR_UNSUPPORTED;
   *bytes = pages_workspace(L, batch, num_queries, list_len, num_splits);
   return PALU_OK;
 }
@@ -792,14 +805,15 @@ palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int
   palu_status s = make_layer(cfg, ranks_k, ranks_k, &L);   // the value ranks play no part
   if (s != PALU_OK) return s;
   if (batch < 0 || max_pages <= 0 || num_pages < 0) return PALU_ERR_INVALID_ARG;
-  if (batch > 65535) return PALU_ERR_UNSUPPORTED;
+  if (batch > 65535 || !countable(cfg, max_pages)) return PALU_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < kStatusBytes) return PALU_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PALU_ERR_ALIGNMENT;
   if (batch == 0) return PALU_OK;
   const bool int4 = cfg->latent_dtype == PALU_INT4;
   if (!zk_pool || !page_table || !seq_lens || !B_k || !bounds || (int4 && !zk_scales) || num_pages == 0)
     return PALU_ERR_INVALID_ARG;
-  if (!aligned16(zk_pool) || !aligned16(B_k) || !aligned16(bounds) || (int4 && !aligned16(zk_scales)))
+  if (!aligned16(zk_pool) || !aligned16(B_k) || !aligned16(bounds) || (int4 && !aligned16(zk_scales)) ||
+      !aligned4({first, pos_pool, page_table, seq_lens}))
     return PALU_ERR_ALIGNMENT;
   palu::GroupMap gm{};
   build_map(L, nullptr, 0, zk_pool, nullptr, zk_scales, nullptr, gm);
@@ -832,7 +846,7 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
     return PALU_ERR_INVALID_ARG;
   const long long G = cfg->num_heads / cfg->group_size;
   if (batch * G * num_queries > PALU_SELECT_MAX_LISTS || batch > 65535 || max_pages > PALU_SELECT_MAX_PAGES ||
-      (long long)cfg->group_size * cfg->head_dim > 8192)
+      !countable(cfg, max_pages) || (long long)cfg->group_size * cfg->head_dim > 8192)
     return PALU_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < palu::select_workspace(cfg, batch, num_queries, max_pages))
     return PALU_ERR_WORKSPACE;
@@ -840,7 +854,9 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
   if (batch == 0) return PALU_OK;
   if (!q || !q_pos || !bounds || !page_table || !seq_lens || !page_list || !page_counts || num_pages == 0)
     return PALU_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(bounds)) return PALU_ERR_ALIGNMENT;
+  if (!aligned16(q) || !aligned16(bounds) ||
+      !aligned4({q_pos, page_table, seq_lens, page_list, page_counts, page_scores}))
+    return PALU_ERR_ALIGNMENT;
   uint64_t omega[palu::kMaxHalfDim];
   fill_omega(cfg, omega);
   return cuda_status(palu::launch_select(cfg, batch, num_queries, q, q_pos, bounds, pos_pool != nullptr, page_table,

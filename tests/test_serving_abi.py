@@ -89,6 +89,35 @@ def test_page_bounds(kw, code):
     assert call("palu_page_bounds", BOUNDS, bounds_args(), **kw) == code
 
 
+@pytest.mark.parametrize("kw", [dict(table=A + 2), dict(lens=A + 2), dict(first=A + 2), dict(pos=A + 1)])
+def test_page_bounds_takes_aligned_words(kw):
+    assert call("palu_page_bounds", BOUNDS, bounds_args(), batch=1, **kw) == ALIGNMENT
+
+
+@pytest.mark.parametrize("kw", [dict(table=A + 2), dict(lens=A + 2), dict(q_pos=A + 2), dict(list=A + 2),
+                                dict(counts=A + 1), dict(scores=A + 2)])
+def test_select_pages_takes_aligned_words(kw):
+    assert call("palu_select_pages", SELECT, select_args(), batch=1, **kw) == ALIGNMENT
+
+
+@pytest.mark.parametrize("kw", [dict(table=A + 2), dict(lens=A + 2), dict(q_pos=A + 2), dict(list=A + 2),
+                                dict(counts=A + 1), dict(lse=A + 2), dict(pos=A + 2), dict(out=A + 8)])
+def test_decode_attn_pages_takes_aligned_words(kw):
+    assert call("palu_decode_attn_pages", ATTEND, attend_args(), batch=1, **kw) == ALIGNMENT
+
+
+def test_token_counts_past_32_bits():
+    wide = 1 << 24                                  # pages of 128 tokens: 2^31 tokens
+    assert call("palu_page_bounds", BOUNDS, bounds_args(), max_pages=wide) == UNSUPPORTED
+    assert call("palu_page_bounds", BOUNDS, bounds_args(), max_pages=wide - 1) == OK
+    assert call("palu_decode_attn_pages", ATTEND, attend_args(), max_pages=wide) == UNSUPPORTED
+    assert call("palu_decode_attn_pages", ATTEND, attend_args(), max_pages=wide - 1) == OK
+    assert call("palu_decode_attn_pages", ATTEND, attend_args(), keep=wide + 1) == UNSUPPORTED
+    big_pages = select_args(page_size=1 << 17)
+    assert call("palu_select_pages", SELECT, big_pages, max_pages=1 << 14) == UNSUPPORTED
+    assert call("palu_select_pages", SELECT, big_pages, max_pages=(1 << 14) - 1) == OK
+
+
 def test_page_bounds_configs():
     assert call("palu_page_bounds", BOUNDS, bounds_args(act_dtype="f16", latent_dtype="int4", rank_v=256), batch=1) == INVALID
     assert call("palu_page_bounds", BOUNDS, bounds_args(rank_k=100)) == ALIGNMENT
@@ -215,3 +244,17 @@ def test_binding_checks_pool_sizes():
     with pytest.raises(ValueError, match="zv_pool holds fewer"):
         P.palu_decode_attn_pages(c, q, i32(1, 1), None, zk[:100], None, None, None, i32(1, 2), i32(1), i32(1, 1, 1, 4),
                                  i32(1, 1, 1), pages, Bk, Bk[:128], q, None, ws())
+
+
+def test_binding_checks_the_number_of_ranks():
+    c = cfg()
+    with pytest.raises(ValueError, match="8 head groups"):
+        P.palu_page_bounds(c, None, None, None, None, i32(0, 2), i32(0), 1, ws(), ws(), ws(), ranks_k=[256] * 7)
+    with pytest.raises(ValueError, match="8 head groups"):
+        P.palu_decode_pages_workspace_size(c, 1, 1, 4, ranks_k=[256] * 8, ranks_v=[128] * 9)
+    with pytest.raises(ValueError, match="together"):
+        P.palu_decode_pages_workspace_size(c, 1, 1, 4, ranks_k=[256] * 8)
+    empty = cfg()
+    empty.group_size = 0
+    with pytest.raises(P.PaluError):
+        P.palu_decode_pages_workspace_size(empty, 1, 1, 4)
