@@ -21,10 +21,24 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowsPerThread = 4;   // rows a thread looks up side by side
+
+// Quotients by the page size, which is known only at run time: n / P = (n·m) >> s for
+// 0 <= n < 2^31 with s = 31 + ceil(log2 P) and m = ceil(2^s / P) (m·P exceeds 2^s by less
+// than P <= 2^(s - 31), so the product is off by less than 1 / P).
+struct Divisor {
+  unsigned long long m;
+  int s;
+};
+Divisor divisor_of(int P) {
+  Divisor d{0, 31};
+  while ((1ull << (d.s - 31)) < (unsigned long long)P) ++d.s;
+  d.m = ((1ull << d.s) + P - 1) / P;
+  return d;
+}
 
 struct PlanArgs {
   int batch, P, max_pages, num_pages, n_rows;
+  Divisor by;
   const int32_t* num_new;
   int32_t* seq_lens;
   int32_t* page_table;
@@ -61,8 +75,29 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return before + s - v;
 }
 
-__device__ __forceinline__ int pages_of(long long tokens, int P) { return (int)((tokens + P - 1) / P); }
+// tokens / P and pages that hold that many (0 <= tokens <= max_pages·P < 2^31).
+__device__ __forceinline__ int page_of(const PlanArgs& a, int tokens) {
+  return (int)(((unsigned long long)(unsigned)tokens * a.by.m) >> a.by.s);
+}
+__device__ __forceinline__ int pages_of(const PlanArgs& a, int tokens) {
+  return tokens > 0 ? page_of(a, tokens - 1) + 1 : 0;
+}
 
+__device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The last i < n with start[i] <= r (start[0] <= r).
+__device__ __forceinline__ int last_from(const int32_t* start, int n, long long r) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// ROWS: consecutive rows a thread looks up side by side.
+template <int ROWS>
 __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
   extern __shared__ int32_t smem[];
   int32_t* start = smem;                  // [batch + 1] first row of each sequence
@@ -95,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
       if (blockIdx.x == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 5000000 + b);
       n = 0;
     }
-    const int had = bad ? 0 : pages_of(L, a.P);
-    int need = bad || !in ? 0 : pages_of(left, a.P) - had;   // negative: pages given back
+    // pages to get, negative: given back
+    int need = bad || !in ? 0 : pages_of(a, (int)left) - pages_of(a, L);
     const long long need_up = need > 0 ? need : 0;
     const long long p0 = through + block_scan(need_up, warp_sums, total);
     through += total;
@@ -123,45 +158,48 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
   }
   __syncthreads();
 
-  // this CTA's rows: kRowsPerThread lookups side by side, so their loads overlap
+  // this CTA's rows, ROWS consecutive ones a thread: the sequence is searched for once and
+  // followed, the table lookups overlap
   const int total_rows = start[a.batch];
-  for (long long r0 = (long long)blockIdx.x * kThreads * kRowsPerThread + tid; r0 < a.n_rows;
-       r0 += (long long)gridDim.x * kThreads * kRowsPerThread) {
-    int b[kRowsPerThread], pos[kRowsPerThread], off[kRowsPerThread], page[kRowsPerThread];
+  const bool wide = aligned16(a.slots) && aligned16(a.positions);
+  for (long long r0 = ((long long)blockIdx.x * kThreads + tid) * ROWS; r0 < a.n_rows;
+       r0 += (long long)gridDim.x * kThreads * ROWS) {
+    int b[ROWS], pos[ROWS], fresh[ROWS], page[ROWS], slot[ROWS];
+    int at = -1;                              // sequence of the last row looked at
 #pragma unroll
-    for (int k = 0; k < kRowsPerThread; ++k) {
-      const long long r = r0 + k * kThreads;
+    for (int k = 0; k < ROWS; ++k) {
+      const long long r = r0 + k;
       b[k] = -1;
-      pos[k] = off[k] = page[k] = 0;
+      pos[k] = fresh[k] = page[k] = 0;
       if (r >= total_rows) continue;
-      int lo = 0, hi = a.batch - 1;         // the last sequence whose first row is <= r
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= r) lo = mid;
-        else hi = mid - 1;
-      }
-      if (take[lo] <= 0) continue;
-      b[k] = lo;
-      pos[k] = len[lo] + (int)(r - start[lo]);
-      const int lp = pos[k] / a.P;
-      off[k] = pos[k] - lp * a.P;
-      const int fresh = lp - pages_of(len[lo], a.P);   // >= 0: a page taken by this call
-      page[k] = fresh >= 0 ? a.free_pages[F - 1 - before[lo] - fresh] : a.page_table[(size_t)lo * a.max_pages + lp];
+      if (at < 0) at = last_from(start, a.batch, r);
+      else if (start[at + 1] <= r) at = start[at + 2] > r ? at + 1 : last_from(start, a.batch, r);
+      if (take[at] <= 0) continue;
+      b[k] = at;
+      pos[k] = len[at] + (int)(r - start[at]);
+      const int lp = page_of(a, pos[k]);
+      fresh[k] = lp - pages_of(a, len[at]);   // >= 0: a page taken by this call
+      page[k] = fresh[k] >= 0 ? a.free_pages[F - 1 - before[at] - fresh[k]]
+                              : a.page_table[(size_t)at * a.max_pages + lp];
     }
 #pragma unroll
-    for (int k = 0; k < kRowsPerThread; ++k) {
-      const long long r = r0 + k * kThreads;
-      if (r >= a.n_rows) continue;
-      int slot = -1;
-      if (b[k] >= 0) {
-        const int lp = pos[k] / a.P;
-        if (off[k] == 0 && lp >= pages_of(len[b[k]], a.P))   // every new page starts with a new token
-          a.page_table[(size_t)b[k] * a.max_pages + lp] = page[k];
-        if (page[k] < 0 || page[k] >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b[k]);
-        else slot = page[k] * a.P + off[k];
+    for (int k = 0; k < ROWS; ++k) {
+      slot[k] = -1;
+      if (b[k] < 0) continue;
+      const int lp = page_of(a, pos[k]), off = pos[k] - lp * a.P;
+      if (off == 0 && fresh[k] >= 0)          // every new page starts with a new token
+        a.page_table[(size_t)b[k] * a.max_pages + lp] = page[k];
+      if (page[k] < 0 || page[k] >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + b[k]);
+      else slot[k] = page[k] * a.P + off;
+    }
+    if (ROWS == 4 && wide && r0 + ROWS <= a.n_rows) {
+      *reinterpret_cast<int4*>(a.slots + r0) = make_int4(slot[0], slot[1 % ROWS], slot[2 % ROWS], slot[3 % ROWS]);
+      *reinterpret_cast<int4*>(a.positions + r0) = make_int4(pos[0], pos[1 % ROWS], pos[2 % ROWS], pos[3 % ROWS]);
+    } else {
+      for (int k = 0; k < ROWS && r0 + k < a.n_rows; ++k) {
+        a.slots[r0 + k] = slot[k];
+        a.positions[r0 + k] = pos[k];
       }
-      a.slots[r] = slot;
-      a.positions[r] = pos[k];
     }
   }
 
@@ -209,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
       const int b = b0 + tid;
       int pages = 0;
       if (b < a.batch && take[b] < 0)
-        pages = pages_of(len[b], a.P) - pages_of((long long)len[b] + take[b], a.P);
+        pages = pages_of(a, len[b]) - pages_of(a, len[b] + take[b]);
       long long total;
       const long long j0 = done + block_scan(pages, warp_sums, total);
       done += total;
@@ -217,13 +255,8 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
     }
     __syncthreads();
     for (long long j = tid; j < given; j += kThreads) {
-      int lo = 0, hi = a.batch - 1;         // the last sequence whose first page is <= j
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= j) lo = mid;
-        else hi = mid - 1;
-      }
-      const int lp = pages_of((long long)len[lo] + take[lo], a.P) + (int)(j - start[lo]);
+      const int lo = last_from(start, a.batch, j);   // the sequence of page j
+      const int lp = pages_of(a, len[lo] + take[lo]) + (int)(j - start[lo]);
       int32_t* entry = a.page_table + (size_t)lo * a.max_pages + lp;
       const int page = *entry;
       *entry = -1;
@@ -238,7 +271,24 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
   if (tid == 0) *a.num_free = (int)min(left + given, (long long)a.num_pages);
 }
 
-size_t smem_bytes(int batch) { return sizeof(int32_t) * (4 * (size_t)batch + 1); }
+// Rows up to which each has a thread of its own (a CTA on every SM).
+constexpr int kSmall = 148 * kThreads;
+
+template <int ROWS>
+cudaError_t launch(const PlanArgs& a, cudaStream_t st) {
+  const size_t smem = sizeof(int32_t) * (4 * (size_t)a.batch + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(plan_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const long long per = (long long)kThreads * ROWS;
+  long long grid = (a.n_rows + per - 1) / per;
+  grid = grid < 1 ? 1 : grid > 8 * 148 ? 8 * 148 : grid;
+  plan_kernel<ROWS><<<(int)grid, kThreads, smem, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -268,20 +318,11 @@ extern "C" palu_status palu_plan_append(int page_size, int batch, int max_pages,
   const void* all[] = {num_new, seq_lens, page_table, free_pages, num_free, slot_mapping, positions, row_starts, taken};
   for (const void* p : all)
     if (!palu::aligned4(p)) return PALU_ERR_ALIGNMENT;
-  palu::PlanArgs a{batch, page_size, max_pages, num_pages, n_rows, num_new, seq_lens, page_table, free_pages,
-                   num_free, slot_mapping, positions, row_starts, taken,
+  palu::PlanArgs a{batch, page_size, max_pages, num_pages, n_rows, palu::divisor_of(page_size), num_new, seq_lens,
+                   page_table, free_pages, num_free, slot_mapping, positions, row_starts, taken,
                    static_cast<palu::DevStatus*>(workspace),
                    reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + 256)};
-  const size_t smem = palu::smem_bytes(batch);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(palu::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return palu::cuda_status(e);
-  }
-  const long long per = (long long)palu::kThreads * palu::kRowsPerThread;
-  long long grid = ((long long)n_rows + per - 1) / per;
-  grid = grid < 1 ? 1 : grid > 8 * 148 ? 8 * 148 : grid;
-  palu::plan_kernel<<<(int)grid, palu::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  palu::count_launch();
-  return palu::cuda_status(cudaGetLastError());
+  const cudaError_t e = n_rows <= palu::kSmall ? palu::launch<1>(a, reinterpret_cast<cudaStream_t>(stream))
+                                               : palu::launch<4>(a, reinterpret_cast<cudaStream_t>(stream));
+  return palu::cuda_status(e);
 }

@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 256;   // entries one partial sum covers: a warp's, 8 a lane
 constexpr int kAhead = 2;     // groups a warp has in flight
+constexpr int kKept = 1024;   // group sums the drawing CTA keeps from its first pass over them
 
 struct VerifyArgs {
   int D, V, share, groups;
@@ -198,10 +199,15 @@ __device__ __forceinline__ double warp_scan(double s) {
 // passes u·total (the last one of positive sum if rounding hides it), then the entry within it.
 // -1: no positive weight.
 template <class R>
-__device__ int draw(const R& row, const double* sums, int groups, int V, float u, double* buf, int* ibuf) {
+__device__ int draw(const R& row, const double* sums, int groups, int V, float u, double* kept, double* buf, int* ibuf) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   double part = 0.0;
-  for (int i = tid; i < groups; i += kThreads) part += __ldcg(sums + i);
+#pragma unroll 4
+  for (int i = tid; i < groups; i += kThreads) {
+    const double s = __ldcg(sums + i);
+    if (i < kKept) kept[i] = s;          // read again by the same thread
+    part += s;
+  }
   const double total = block_sum(part, buf);
   if (!(total > 0.0)) return -1;
   const double at = (double)u * total;
@@ -213,7 +219,7 @@ __device__ int draw(const R& row, const double* sums, int groups, int V, float u
   int won = -1;
   for (int g0 = 0; g0 < groups; g0 += kThreads) {
     const int i = g0 + tid;
-    const double s = i < groups ? __ldcg(sums + i) : 0.0;
+    const double s = i >= groups ? 0.0 : i < kKept ? kept[i] : __ldcg(sums + i);
     const double upto = warp_scan(s);
     if (lane == 31) buf[warp] = upto;
     __syncthreads();
@@ -246,7 +252,7 @@ __device__ int draw(const R& row, const double* sums, int groups, int V, float u
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   using T = typename Dt<DT>::T;
-  __shared__ double buf[kWarps];
+  __shared__ double buf[kWarps], kept[kKept];
   __shared__ int ibuf[3];
   __shared__ int accepted, is_last;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -255,6 +261,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     if (blockIdx.x == 0 && tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 1000000 + b);
     n = n < 0 ? 0 : a.D;
   }
+  const float u = a.u_sample[b];   // wanted at the very end: its load must not wait until then
   const T* target = static_cast<const T*>(a.target) + (size_t)b * (a.D + 1) * a.target_ld;
   const T* draft = a.draft != nullptr ? static_cast<const T*>(a.draft) + (size_t)b * a.D * a.draft_ld : nullptr;
   const int32_t* xs = a.draft_tokens + (size_t)b * a.D;
@@ -262,13 +269,13 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     bool yes = false;
     if (tid < a.D) {
       const int x = xs[tid];                                    // independent of n: its load overlaps n's
-      const float u = a.u_accept[(size_t)b * a.D + tid];
+      const float ua = a.u_accept[(size_t)b * a.D + tid];
       const bool in = x >= 0 && x < a.V;
       if (!in && tid < n && blockIdx.x == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 2000000 + b);
       if (in) {
         const double p = (double)Dt<DT>::to_f(target[(size_t)tid * a.target_ld + x]);
         const double q = draft != nullptr ? (double)Dt<DT>::to_f(draft[(size_t)tid * a.draft_ld + x]) : 1.0;
-        yes = tid < n && (double)u * q < p;
+        yes = tid < n && (double)ua * q < p;
       }
     }
     const unsigned no = ~__ballot_sync(0xffffffffu, yes);
@@ -305,8 +312,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     __syncthreads();
   }
   // the sequence's last CTA draws the token
-  const float u = a.u_sample[b];
-  int hit = draw(row, sums, a.groups, a.V, u, buf, ibuf);
+  int hit = draw(row, sums, a.groups, a.V, u, kept, buf, ibuf);
   if (hit < 0 && refused) {
     // p <= q everywhere: the target's own row
     row.q = nullptr;
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
     sum_groups(0, a.groups);
     __threadfence();
     __syncthreads();
-    hit = draw(row, sums, a.groups, a.V, u, buf, ibuf);
+    hit = draw(row, sums, a.groups, a.V, u, kept, buf, ibuf);
   }
   for (int i = tid; i <= a.D; i += kThreads)
     a.tokens[(size_t)b * (a.D + 1) + i] = i < acc ? xs[i] : i == acc ? hit : -1;
