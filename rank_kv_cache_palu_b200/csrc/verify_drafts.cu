@@ -25,7 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 256;   // entries one partial sum covers: a warp's, 8 a lane
-constexpr int kAhead = 2;     // groups a warp has in flight
 constexpr int kKept = 1024;   // group sums the drawing CTA keeps from its first pass over them
 
 struct VerifyArgs {
@@ -103,45 +102,49 @@ struct Row {
     for (int k = 0; k < 8; ++k) s += weight_of(a[k], b[k]);
     return s;
   }
-  // Σ weights of this lane's 8 entries of the group of 256 that starts at v0, which lies whole in the row
-  __device__ __forceinline__ double lane_sum(int v0) const {
+  // This lane's 8 entries of the group of 256 that starts at v0, which lies whole in the row.
+  struct Raw {
+    uint4 a[8 * sizeof(T) / 16], b[8 * sizeof(T) / 16];
+  };
+  __device__ __forceinline__ void load(int v0, Raw& raw) const {
     const int lane = threadIdx.x & 31;
-    float a[8], b[8];
-    int at[8];
     if constexpr (VEC) {
-      constexpr int kWords = 8 * sizeof(T) / 16;
-      uint4 ra[kWords], rb[kWords];
 #pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        ra[w] = __ldg(reinterpret_cast<const uint4*>(p + v0 + 8 * lane) + w);
-        rb[w] = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q + v0 + 8 * lane) + w) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        a[k] = Dt<DT>::to_f(reinterpret_cast<const T*>(ra)[k]);
-        b[k] = Dt<DT>::to_f(reinterpret_cast<const T*>(rb)[k]);
-        at[k] = v0 + 8 * lane + k;
+      for (int w = 0; w < 8 * (int)sizeof(T) / 16; ++w) {
+        raw.a[w] = __ldg(reinterpret_cast<const uint4*>(p + v0 + 8 * lane) + w);
+        raw.b[w] = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q + v0 + 8 * lane) + w) : make_uint4(0, 0, 0, 0);
       }
     } else {
+      T* a = reinterpret_cast<T*>(raw.a);
+      T* b = reinterpret_cast<T*>(raw.b);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        at[k] = v0 + 32 * k + lane;
-        a[k] = Dt<DT>::to_f(p[at[k]]);
-        b[k] = q != nullptr ? Dt<DT>::to_f(q[at[k]]) : 0.f;
+        a[k] = p[v0 + 32 * k + lane];
+        b[k] = q != nullptr ? q[v0 + 32 * k + lane] : Dt<DT>::from_f(0.f);
       }
     }
-    if (x >= 0) {
+  }
+  __device__ __forceinline__ double lane_sum(int v0, const Raw& raw) const {
+    const int lane = threadIdx.x & 31;
+    float a[8], b[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      a[k] = Dt<DT>::to_f(reinterpret_cast<const T*>(raw.a)[k]);
+      b[k] = Dt<DT>::to_f(reinterpret_cast<const T*>(raw.b)[k]);
+    }
+    if (x >= v0 && x < v0 + kGroup) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (at[k] == x) b[k] = 1.f;
+        if ((VEC ? v0 + 8 * lane + k : v0 + 32 * k + lane) == x) b[k] = 1.f;
     }
     return sum_of(a, b);
   }
-  // Σ weights of the group of 256 entries that starts at v0 (the whole warp takes part and gets it)
-  __device__ __forceinline__ double group_sum(int v0, int V) const {
+  // Σ weights of the group of 256 entries that starts at v0, loaded if it is a whole one (the whole
+  // warp takes part and gets it)
+  __device__ __forceinline__ double group_sum(int v0, int V, const Raw& raw) const {
     double s = 0.0;
     if (v0 + kGroup <= V) {
-      s = lane_sum(v0);
+      s = lane_sum(v0, raw);
     } else {
       const int v = v0 + 8 * ((int)threadIdx.x & 31);
 #pragma unroll
@@ -250,7 +253,7 @@ __device__ int draw(const R& row, const double* sums, int groups, int V, float u
 }
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a) {
   using T = typename Dt<DT>::T;
   __shared__ double buf[kWarps], kept[kKept];
   __shared__ int ibuf[3];
@@ -289,14 +292,28 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   row.q = refused && draft != nullptr ? draft + (size_t)acc * a.draft_ld : nullptr;
   row.x = refused && draft == nullptr ? xs[acc] : -1;
   double* sums = a.sums + (size_t)b * a.groups;
-  auto sum_groups = [&](int g0, int g1) {      // kAhead groups a warp side by side
-    for (int g = g0 + warp * kAhead; g < g1; g += kWarps * kAhead) {
-      double s[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) s[k] = g + k < g1 ? row.group_sum((g + k) * kGroup, a.V) : 0.0;
+  // each warp kAhead groups at a time, the next ones on their way meanwhile
+  auto sum_groups = [&](int g0, int g1) {
+    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
+    using Raw = typename Row<DT, VEC>::Raw;
+    Raw now[kAhead], next[kAhead];
+    auto load = [&](int g, Raw* raw) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
+        if (g + k < g1 && (g + k + 1) * kGroup <= a.V) row.load((g + k) * kGroup, raw[k]);
+    };
+    int g = g0 + warp * kAhead;
+    load(g, now);
+    for (; g < g1; g += kWarps * kAhead) {
+      load(g + kWarps * kAhead, next);
+      double s[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s[k] = g + k < g1 ? row.group_sum((g + k) * kGroup, a.V, now[k]) : 0.0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
         if (lane == 0 && g + k < g1) sums[g + k] = s[k];
+        now[k] = next[k];
+      }
     }
   };
   sum_groups(blockIdx.x * a.share, min(a.groups, (int)(blockIdx.x + 1) * a.share));
