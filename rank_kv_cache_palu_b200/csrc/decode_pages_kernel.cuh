@@ -24,6 +24,12 @@
 namespace palu {
 namespace {
 
+// Shared-memory descriptor `bytes` further on (a multiple of 16; shared memory ends below the 18 bits of
+// its address field): one addition where building a descriptor takes a dozen instructions.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  return (desc & 0xffffffff00000000ull) | ((uint32_t)desc + (bytes >> 4));
+}
+
 struct PagesSmem {
   uint32_t zk, zv, p, qr, psc, tb, red, bars, tmem_slot, abort, tiles, b, total;
 };
@@ -657,7 +663,11 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         constexpr int kBf = ACT == PALU_BF16 ? 1 : 0;
         const uint32_t idesc_d = idesc_f16(kBf, 0, 1, 256, 128);    // z_k K-major, B_k MN-major
         const uint32_t idesc_pv = idesc_f16(kBf, 1, 0, 16, 128);    // z_vᵀ MN-major, Pᵀ K-major
-        const uint32_t b_lbo = (uint32_t)r_k * 128;                  // bytes between 64-column blocks of B
+        // operand descriptors at the first stage, chunk or buffer: the others lie a multiple of 16 bytes on
+        const uint64_t zk0 = sdesc(base + L.zk, 16, kZkSbo, kZkSwz);
+        const uint64_t b0 = sdesc(base + L.b, (uint32_t)r_k * 128, 1024, kSw128);   // 64-column blocks of B
+        const uint64_t zv0 = sdesc(base + L.zv, kInt4 ? kZvBytes / 2 : kZvBytes, 1024, kSw128);
+        const uint64_t p0 = sdesc(base + L.p, 16, 1024, kSw128);
         int zs = 0;
         uint32_t zph = 0, vph = 0;
         // timeout-path test hook: first wait on a phase nothing completes before the teardown commit
@@ -698,17 +708,15 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         auto issue_pv_block = [&]() {
           const int j = pv_next;
           tc_fence_after();
-          const uint32_t p_base = base + L.p + (uint32_t)(j & 1) * kPBytes;
+          const uint64_t p = desc_at(p0, (uint32_t)(j & 1) * kPBytes);
           if constexpr (kInt4) {
             const int mb = pv_s >> 1, th = pv_s & 1;
             const uint32_t a_tmem = tmem + (uint32_t)((j + 1) & 1) * 256 + (uint32_t)mb * 32;
-            const uint32_t z_base = base + L.zv + (uint32_t)vs * kZvBytes;
+            const uint64_t z = desc_at(zv0, (uint32_t)vs * kZvBytes), ph = desc_at(p, th * 2048);
   #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               // rows = latent entries, K = 16 tokens of the half
-              const uint64_t ad = sdesc(z_base + kk * 16 * 128, kZvBytes / 2, 1024, kSw128);
-              const uint64_t bd = sdesc(p_base + th * 2048 + kk * 32, 16, 1024, kSw128);
-              umma_f16(a_tmem, ad, bd, idesc_pv, (th | kk) != 0);
+              umma_f16(a_tmem, desc_at(z, kk * 16 * 128), desc_at(ph, kk * 32), idesc_pv, (th | kk) != 0);
             }
             umma_commit(bar(BAR_ZV_EMPTY + vs));
             if (++vs == kNVS) { vs = 0; vph ^= 1; }
@@ -719,9 +727,8 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
   #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk) {
               // rows = latent entries (two 64-entry blocks, one per stage), K = tokens
-              const uint64_t ad = sdesc(base + L.zv + kk * 16 * 128, kZvBytes, 1024, kSw128);
-              const uint64_t bd = sdesc(p_base + (kk >> 2) * 2048 + (kk & 3) * 32, 16, 1024, kSw128);
-              umma_f16(a_tmem, ad, bd, idesc_pv, kk != 0);
+              umma_f16(a_tmem, desc_at(zv0, kk * 16 * 128), desc_at(p, (kk >> 2) * 2048 + (kk & 3) * 32), idesc_pv,
+                       kk != 0);
             }
             umma_commit(bar(BAR_ZV_EMPTY + 0));
             umma_commit(bar(BAR_ZV_EMPTY + 1));
@@ -764,13 +771,10 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
           for (int c = 0; c < nkc; ++c) {
             if (!poll_wait(bar(BAR_ZK_FULL + zs), zph, 24)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t zk_addr = base + L.zk + zs * kZkBytes;
-            const uint32_t b_addr = base + L.b + (uint32_t)c * kChunk * 128;
+            const uint64_t z = desc_at(zk0, (uint32_t)zs * kZkBytes), b = desc_at(b0, (uint32_t)c * kChunk * 128);
   #pragma unroll
             for (int kk = 0; kk < kChunk / 16; ++kk) {
-              const uint64_t ad = sdesc(zk_addr + kk * 32, 16, kZkSbo, kZkSwz);
-              const uint64_t bd = sdesc(b_addr + kk * 16 * 128, b_lbo, 1024, kSw128);
-              umma_f16(d_tmem, ad, bd, idesc_d, (c | kk) != 0);
+              umma_f16(d_tmem, desc_at(z, kk * 32), desc_at(b, kk * 16 * 128), idesc_d, (c | kk) != 0);
             }
             umma_commit(bar(BAR_ZK_EMPTY + zs));
             if (++zs == kNZK) { zs = 0; zph ^= 1; }
