@@ -24,6 +24,13 @@
 namespace palu {
 namespace {
 
+// True on one lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory descriptor `bytes` further on (a multiple of 16; shared memory ends below the 18 bits of
 // its address field): one addition where building a descriptor takes a dozen instructions.
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
@@ -659,7 +666,12 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       }
     } else if (warp == 1) {
       // ============================================================ MMA issuer
-      if (lane == 0) {
+      // The whole warp goes through the loop, one lane issues: what the loop computes is then known to
+      // be the same on every lane and stays in the registers the MMAs take their operands from.
+      {
+        const bool leader = elect_one();
+        auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(b, parity)) != 0; };
+        auto gave_up = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
         constexpr int kBf = ACT == PALU_BF16 ? 1 : 0;
         const uint32_t idesc_d = idesc_f16(kBf, 0, 1, 256, 128);    // z_k K-major, B_k MN-major
         const uint32_t idesc_pv = idesc_f16(kBf, 1, 0, 16, 128);    // z_vᵀ MN-major, Pᵀ K-major
@@ -673,6 +685,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         // timeout-path test hook: first wait on a phase nothing completes before the teardown commit
         bool ok = a.stall_test == 0 || mbar_wait(bar(BAR_TEARDOWN), 0, abort_flag, st, 26);
         ok = ok && mbar_wait(bar(BAR_B), 0, abort_flag, st, 20);
+        ok = __all_sync(0xffffffffu, ok);
         int pv_next = 0;       // next tile whose value MMA is not issued yet
         int pv_s = 0;          // next operand of that value MMA: block mb = pv_s / 2 (int4: token half pv_s % 2)
         int vs = 0;            // int4: z_v ring stage of that operand
@@ -683,9 +696,9 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         // round trip never holds a slot back from the next key MMA.  The last tile's value
         // MMA goes into the other slot once it is free.  Its gate (besides P and z_v):
         auto pv_gate = [&](int j) -> bool {
-          if (j + 1 < N) return mbar_test_wait(bar(BAR_MID), (uint32_t)((j + 1) & 1));
+          if (j + 1 < N) return ready(bar(BAR_MID), (uint32_t)((j + 1) & 1));
           const int u = j + 1;
-          return mbar_test_wait(bar(BAR_D_EMPTY + (u & 1)), (uint32_t)(((u >> 1) & 1) ^ 1));
+          return ready(bar(BAR_D_EMPTY + (u & 1)), (uint32_t)(((u >> 1) & 1) ^ 1));
         };
         // The next stage of the pending value MMA can go?  (Phases cannot alias: the epilogue
         // cannot pass tile j + 1 before the value sums of tile j are folded.)  int4: one ring
@@ -693,12 +706,12 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         // 64-entry halves of operand mb over all 128 tokens.
         auto pv_ready = [&]() -> bool {
           if constexpr (kInt4) {
-            if (!mbar_test_wait(bar(BAR_ZV_FULL + vs), vph)) return false;
+            if (!ready(bar(BAR_ZV_FULL + vs), vph)) return false;
           } else {
-            if (!(mbar_test_wait(bar(BAR_ZV_FULL + 0), vph) && mbar_test_wait(bar(BAR_ZV_FULL + 1), vph)))
+            if (!(ready(bar(BAR_ZV_FULL + 0), vph) && ready(bar(BAR_ZV_FULL + 1), vph)))
               return false;
           }
-          return pv_s > 0 || (mbar_test_wait(bar(BAR_P_FULL + (pv_next & 1)), (uint32_t)((pv_next >> 1) & 1)) &&
+          return pv_s > 0 || (ready(bar(BAR_P_FULL + (pv_next & 1)), (uint32_t)((pv_next >> 1) & 1)) &&
                               pv_gate(pv_next));
         };
         // One value-MMA operand into block mb of the value sums.  int4: stage (mb, th) =
@@ -713,30 +726,30 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
             const int mb = pv_s >> 1, th = pv_s & 1;
             const uint32_t a_tmem = tmem + (uint32_t)((j + 1) & 1) * 256 + (uint32_t)mb * 32;
             const uint64_t z = desc_at(zv0, (uint32_t)vs * kZvBytes), ph = desc_at(p, th * 2048);
-  #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              // rows = latent entries, K = 16 tokens of the half
-              umma_f16(a_tmem, desc_at(z, kk * 16 * 128), desc_at(ph, kk * 32), idesc_pv, (th | kk) != 0);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)    // rows = latent entries, K = 16 tokens of the half
+                umma_f16(a_tmem, desc_at(z, kk * 16 * 128), desc_at(ph, kk * 32), idesc_pv, (th | kk) != 0);
+              umma_commit(bar(BAR_ZV_EMPTY + vs));
             }
-            umma_commit(bar(BAR_ZV_EMPTY + vs));
             if (++vs == kNVS) { vs = 0; vph ^= 1; }
             ++pv_s;
           } else {
             static_assert(kInt4 || zv_stages(false) == 2, "one value MMA operand = the two ring stages");
             const uint32_t a_tmem = tmem + (uint32_t)((j + 1) & 1) * 256 + (uint32_t)(pv_s >> 1) * 32;
-  #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk) {
-              // rows = latent entries (two 64-entry blocks, one per stage), K = tokens
-              umma_f16(a_tmem, desc_at(zv0, kk * 16 * 128), desc_at(p, (kk >> 2) * 2048 + (kk & 3) * 32), idesc_pv,
-                       kk != 0);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)    // rows = latent entries (two 64-entry blocks, one per stage), K = tokens
+                umma_f16(a_tmem, desc_at(zv0, kk * 16 * 128), desc_at(p, (kk >> 2) * 2048 + (kk & 3) * 32), idesc_pv,
+                         kk != 0);
+              umma_commit(bar(BAR_ZV_EMPTY + 0));
+              umma_commit(bar(BAR_ZV_EMPTY + 1));
             }
-            umma_commit(bar(BAR_ZV_EMPTY + 0));
-            umma_commit(bar(BAR_ZV_EMPTY + 1));
             vph ^= 1;
             pv_s += 2;
           }
           if (pv_s == 2 * NRV) {
-            umma_commit(bar(BAR_AT_FULL));
+            if (leader) umma_commit(bar(BAR_AT_FULL));
             ++pv_next;
             pv_s = 0;
           }
@@ -751,12 +764,12 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         auto poll_wait = [&](uint32_t b, uint32_t parity, int where) -> bool {
           const long long t0 = clock64();
           while (true) {
-            if (mbar_test_wait(b, parity)) return true;
+            if (ready(b, parity)) return true;
             if (pv_step()) continue;
-            if (*abort_flag) return false;
+            if (gave_up()) return false;
             __nanosleep(64);   // leave the issue slots of this SM partition to the epilogue warps
-            if (clock64() - t0 > wait_limit(abort_flag)) {
-              report(st, PALU_ERR_DEVICE_TIMEOUT, where);
+            if (__any_sync(0xffffffffu, clock64() - t0 > wait_limit(abort_flag))) {
+              if (leader) report(st, PALU_ERR_DEVICE_TIMEOUT, where);
               *abort_flag = 1;
               return false;
             }
@@ -772,25 +785,26 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
             if (!poll_wait(bar(BAR_ZK_FULL + zs), zph, 24)) { ok = false; break; }
             tc_fence_after();
             const uint64_t z = desc_at(zk0, (uint32_t)zs * kZkBytes), b = desc_at(b0, (uint32_t)c * kChunk * 128);
-  #pragma unroll
-            for (int kk = 0; kk < kChunk / 16; ++kk) {
-              umma_f16(d_tmem, desc_at(z, kk * 32), desc_at(b, kk * 16 * 128), idesc_d, (c | kk) != 0);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < kChunk / 16; ++kk)
+                umma_f16(d_tmem, desc_at(z, kk * 32), desc_at(b, kk * 16 * 128), idesc_d, (c | kk) != 0);
+              umma_commit(bar(BAR_ZK_EMPTY + zs));
             }
-            umma_commit(bar(BAR_ZK_EMPTY + zs));
             if (++zs == kNZK) { zs = 0; zph ^= 1; }
           }
           if (!ok) break;
-          umma_commit(bar(BAR_D_FULL + slot));
+          if (leader) umma_commit(bar(BAR_D_FULL + slot));
         }
         // the value MMAs still pending (the last tiles'), each once its operands are in
         if (ok) {
           const long long t0 = clock64();
           while (pv_next < N) {
             if (pv_step()) continue;
-            if (*abort_flag) break;
+            if (gave_up()) break;
             __nanosleep(64);
-            if (clock64() - t0 > wait_limit(abort_flag)) {
-              report(st, PALU_ERR_DEVICE_TIMEOUT, 21);
+            if (__any_sync(0xffffffffu, clock64() - t0 > wait_limit(abort_flag))) {
+              if (leader) report(st, PALU_ERR_DEVICE_TIMEOUT, 21);
               *abort_flag = 1;
               break;
             }
@@ -798,7 +812,8 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         }
         // drain, also after an abort: every MMA issued above has completed before
         // TMEM is released, and the B_k load has landed before the CTA exits
-        umma_commit(bar(BAR_TEARDOWN));
+        if (leader) umma_commit(bar(BAR_TEARDOWN));
+        __syncwarp();
         mbar_drain(bar(BAR_TEARDOWN), 0, st, 25);
         mbar_drain(bar(BAR_B), 0, st, 20);
       }
