@@ -210,72 +210,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
-    if (lane == 0) {
-      constexpr int kBf = ACT == PALU_BF16 ? 1 : 0;
-      const uint32_t idesc_s = idesc_f16(kBf, 0, 0, kN, 128);    // z_k K-major, q̃ K-major
-      const uint32_t idesc_pv = idesc_f16(kBf, 1, 0, kNP, 128);  // z_vᵀ MN-major, Pᵀ K-major
-      int zs = 0, vs = 0, seg = -1;
-      uint32_t zph = 0, vph = 0;
-      // timeout-path test hook: first wait on a phase nothing completes before the teardown commit
-      bool ok = a.stall_test == 0 || mbar_wait(bar(F_TEARDOWN), 0, abort_flag, st, 27);
-      auto issue_pv = [&](int j) -> bool {
-        const int vb = j & 1;
-        const uint32_t a_tmem = tmem + kAt + (uint32_t)vb * NRV * kNP;
-        const uint32_t p_base = base + L.p + (uint32_t)(j & 1) * kPBytes;
-        if (!mbar_wait(bar(F_P_FULL + vb), (j >> 1) & 1, abort_flag, st, 21)) return false;
-        if (!mbar_wait(bar(F_AT_EMPTY + vb), ((j >> 1) & 1) ^ 1, abort_flag, st, 22)) return false;
+    // The whole warp goes through the loop, one lane issues: what the loop computes is then known to
+    // be the same on every lane and stays in the registers the MMAs take their operands from.
+    const bool leader = elect_one();
+    constexpr int kBf = ACT == PALU_BF16 ? 1 : 0;
+    const uint32_t idesc_s = idesc_f16(kBf, 0, 0, kN, 128);    // z_k K-major, q̃ K-major
+    const uint32_t idesc_pv = idesc_f16(kBf, 1, 0, kNP, 128);  // z_vᵀ MN-major, Pᵀ K-major
+    // operand descriptors at the first stage or buffer: the others lie a multiple of 16 bytes on
+    const uint64_t zk0 = sdesc(base + L.zk, 16, 1024, kSw128), q0 = sdesc(base + L.qt, 16, 1024, kSw128);
+    const uint64_t zv0 = sdesc(base + L.zv, kStageBytes, 1024, kSw128), p0 = sdesc(base + L.p, 16, 1024, kSw128);
+    auto wait = [&](int i, uint32_t parity, int where) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, st, where)) != 0;
+    };
+    int zs = 0, vs = 0, seg = -1;
+    uint32_t zph = 0, vph = 0;
+    // timeout-path test hook: first wait on a phase nothing completes before the teardown commit
+    bool ok = a.stall_test == 0 || wait(F_TEARDOWN, 0, 27);
+    auto issue_pv = [&](int j) -> bool {
+      const int vb = j & 1;
+      const uint32_t a_tmem = tmem + kAt + (uint32_t)vb * NRV * kNP;
+      const uint64_t p = desc_at(p0, (uint32_t)vb * kPBytes);
+      if (!wait(F_P_FULL + vb, (j >> 1) & 1, 21)) return false;
+      if (!wait(F_AT_EMPTY + vb, ((j >> 1) & 1) ^ 1, 22)) return false;
+      for (int mb = 0; mb < NRV; ++mb) {
+        for (int cb = 0; cb < 2; ++cb)
+          if (!wait(F_ZV_FULL + vs + cb, vph, 23)) return false;
         tc_fence_after();
-        for (int mb = 0; mb < NRV; ++mb) {
-          for (int cb = 0; cb < 2; ++cb)
-            if (!mbar_wait(bar(F_ZV_FULL + vs + cb), vph, abort_flag, st, 23)) return false;
-          tc_fence_after();
+        const uint64_t z = desc_at(zv0, (uint32_t)vs * kStageBytes);
+        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk) {
-            const uint64_t ad = sdesc(base + L.zv + vs * kStageBytes + kk * 16 * 128, kStageBytes, 1024, kSw128);
-            const uint64_t bd = sdesc(p_base + (kk >> 2) * kNP * 128 + (kk & 3) * 32, 16, 1024, kSw128);
-            umma_f16(a_tmem + mb * kNP, ad, bd, idesc_pv, kk != 0);
-          }
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_f16(a_tmem + mb * kNP, desc_at(z, kk * 16 * 128), desc_at(p, (kk >> 2) * kNP * 128 + (kk & 3) * 32),
+                     idesc_pv, kk != 0);
           umma_commit(bar(F_ZV_EMPTY + vs));
           umma_commit(bar(F_ZV_EMPTY + vs + 1));
-          vs += 2;
-          if (vs == kNZV) { vs = 0; vph ^= 1; }
         }
-        umma_commit(bar(F_AT_FULL + vb));
-        return true;
-      };
-      for (int k = 0; k < N && ok; ++k) {
-        const int slot = k & 1;
-        if (tiles[k].info & kTileFirst) {
-          ++seg;
-          if (!mbar_wait(bar(F_QT_FULL + seg % kNQ), (seg / kNQ) & 1, abort_flag, st, 28)) { ok = false; break; }
-        }
-        if (!mbar_wait(bar(F_D_EMPTY + slot), ((k >> 1) & 1) ^ 1, abort_flag, st, 24)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)slot * kN;
-        const uint32_t q_base = base + L.qt + (uint32_t)(seg % kNQ) * qt_bytes;
-        for (int c = 0; c < nkc; ++c) {
-          if (!mbar_wait(bar(F_ZK_FULL + zs), zph, abort_flag, st, 25)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kChunk / 16; ++kk) {
-            const uint64_t ad = sdesc(base + L.zk + zs * kStageBytes + kk * 32, 16, 1024, kSw128);
-            const uint64_t bd = sdesc(q_base + c * (kN * 128) + kk * 32, 16, 1024, kSw128);
-            umma_f16(d_tmem, ad, bd, idesc_s, (c | kk) != 0);
-          }
-          umma_commit(bar(F_ZK_EMPTY + zs));
-          if (++zs == kNZK) { zs = 0; zph ^= 1; }
-        }
-        if (!ok) break;
-        umma_commit(bar(F_D_FULL + slot));
-        if (tiles[k].info & kTileLast) umma_commit(bar(F_QT_EMPTY + seg % kNQ));
-        // the previous tile's value MMA, once its P is written
-        if (k >= 1 && !issue_pv(k - 1)) { ok = false; break; }
+        vs += 2;
+        if (vs == kNZV) { vs = 0; vph ^= 1; }
       }
-      if (ok && N >= 1) issue_pv(N - 1);
-      // drain, also after an abort: every MMA issued above completes before TMEM is released
-      umma_commit(bar(F_TEARDOWN));
-      mbar_drain(bar(F_TEARDOWN), 0, st, 26);
+      if (leader) umma_commit(bar(F_AT_FULL + vb));
+      return true;
+    };
+    for (int k = 0; k < N && ok; ++k) {
+      const int slot = k & 1;
+      const int info = __shfl_sync(0xffffffffu, tiles[k].info, 0);
+      if (info & kTileFirst) {
+        ++seg;
+        if (!wait(F_QT_FULL + seg % kNQ, (seg / kNQ) & 1, 28)) { ok = false; break; }
+      }
+      if (!wait(F_D_EMPTY + slot, ((k >> 1) & 1) ^ 1, 24)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem + (uint32_t)slot * kN;
+      const uint64_t q = desc_at(q0, (uint32_t)(seg % kNQ) * qt_bytes);
+      for (int c = 0; c < nkc; ++c) {
+        if (!wait(F_ZK_FULL + zs, zph, 25)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t z = desc_at(zk0, (uint32_t)zs * kStageBytes), qc = desc_at(q, (uint32_t)c * kN * 128);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            umma_f16(d_tmem, desc_at(z, kk * 32), desc_at(qc, kk * 32), idesc_s, (c | kk) != 0);
+          umma_commit(bar(F_ZK_EMPTY + zs));
+        }
+        if (++zs == kNZK) { zs = 0; zph ^= 1; }
+      }
+      if (!ok) break;
+      if (leader) {
+        umma_commit(bar(F_D_FULL + slot));
+        if (info & kTileLast) umma_commit(bar(F_QT_EMPTY + seg % kNQ));
+      }
+      // the previous tile's value MMA, once its P is written
+      if (k >= 1 && !issue_pv(k - 1)) { ok = false; break; }
     }
+    if (ok && N >= 1) issue_pv(N - 1);
+    // drain, also after an abort: every MMA issued above completes before TMEM is released
+    if (leader) umma_commit(bar(F_TEARDOWN));
+    __syncwarp();
+    mbar_drain(bar(F_TEARDOWN), 0, st, 26);
   } else {
     // ============================================================ epilogue (warps 2-5)
     // One thread per token row (scores) and per latent row (value sums).

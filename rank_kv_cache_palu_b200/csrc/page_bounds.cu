@@ -483,44 +483,50 @@ __global__ void __launch_bounds__(LAT == PALU_INT4 ? 512 : 384, 1)
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
-    if (lane == 0) {
-      constexpr int kBf = ACT == PALU_BF16 ? 1 : 0;
-      const uint32_t idesc = idesc_f16(kBf, 1, 0, 128, 128);   // B_kᵀ MN-major, z_kᵀ K-major
-      const uint32_t lbo = 2u * (uint32_t)r_k * 128;            // the same half of the second head: two blocks on
-      int zs = 0;
-      uint32_t zph = 0;
-      // timeout-path test hook: first wait on a phase nothing completes before the teardown commit
-      bool ok = a.stall_test == 0 || mbar_wait(bar(B_TEARDOWN), 0, abort_flag, a.st, 45);
-      ok = ok && mbar_wait(bar(B_BK), 0, abort_flag, a.st, 46);
-      for (int k = 0; k < n_items && ok; ++k) {
-        const int slot = k & 1;
-        if (!mbar_wait(bar(B_D_EMPTY + slot), ((k >> 1) & 1) ^ 1, abort_flag, a.st, 47)) { ok = false; break; }
+    // The whole warp goes through the loop, one lane issues: what the loop computes is then known to
+    // be the same on every lane and stays in the registers the MMAs take their operands from.
+    const bool leader = elect_one();
+    constexpr int kBf = ACT == PALU_BF16 ? 1 : 0;
+    const uint32_t idesc = idesc_f16(kBf, 1, 0, 128, 128);   // B_kᵀ MN-major, z_kᵀ K-major
+    // operand descriptors at the first stage and chunk: the same half of the second head lies two blocks on
+    const uint64_t z0 = sdesc(base + L.zk, 16, kZkSbo, kZkSwz);
+    const uint64_t b0 = sdesc(base + L.b, 2u * (uint32_t)r_k * 128, 1024, kSw128);
+    auto wait = [&](int i, uint32_t parity, int where) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, a.st, where)) != 0;
+    };
+    int zs = 0;
+    uint32_t zph = 0;
+    // timeout-path test hook: first wait on a phase nothing completes before the teardown commit
+    bool ok = a.stall_test == 0 || wait(B_TEARDOWN, 0, 45);
+    ok = ok && wait(B_BK, 0, 46);
+    for (int k = 0; k < n_items && ok; ++k) {
+      const int slot = k & 1;
+      if (!wait(B_D_EMPTY + slot, ((k >> 1) & 1) ^ 1, 47)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)slot * kSlotCols;
+      for (int c = 0; c < nkc; ++c) {
+        if (!wait(B_ZK_FULL + zs, zph, 48)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)slot * kSlotCols;
-        for (int c = 0; c < nkc; ++c) {
-          if (!mbar_wait(bar(B_ZK_FULL + zs), zph, abort_flag, a.st, 48)) { ok = false; break; }
-          tc_fence_after();
+        const uint64_t z = desc_at(z0, (uint32_t)zs * kZkBytes), b = desc_at(b0, (uint32_t)c * kChunk * 128);
+        const uint64_t b_hi = desc_at(b, (uint32_t)r_k * 128);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kChunk / 16; ++kk) {
-            const uint64_t zd = sdesc(base + L.zk + zs * kZkBytes + kk * 32, 16, kZkSbo, kZkSwz);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint64_t bd =
-                  sdesc(base + L.b + (uint32_t)hf * r_k * 128 + (uint32_t)(c * kChunk + kk * 16) * 128, lbo, 1024, kSw128);
-              umma_f16(d + hf * 128, bd, zd, idesc, (c | kk) != 0);
-            }
+            umma_f16(d, desc_at(b, kk * 16 * 128), desc_at(z, kk * 32), idesc, (c | kk) != 0);
+            umma_f16(d + 128, desc_at(b_hi, kk * 16 * 128), desc_at(z, kk * 32), idesc, (c | kk) != 0);
           }
           umma_commit(bar(B_ZK_EMPTY + zs));
-          if (++zs == kNZ) { zs = 0; zph ^= 1; }
         }
-        if (!ok) break;
-        umma_commit(bar(B_D_FULL + slot));
+        if (++zs == kNZ) { zs = 0; zph ^= 1; }
       }
-      // drain, also after an abort: MMAs complete before TMEM is released, the B_k load before the CTA exits
-      umma_commit(bar(B_TEARDOWN));
-      mbar_drain(bar(B_TEARDOWN), 0, a.st, 45);
-      mbar_drain(bar(B_BK), 0, a.st, 46);
+      if (!ok) break;
+      if (leader) umma_commit(bar(B_D_FULL + slot));
     }
+    // drain, also after an abort: MMAs complete before TMEM is released, the B_k load before the CTA exits
+    if (leader) umma_commit(bar(B_TEARDOWN));
+    __syncwarp();
+    mbar_drain(bar(B_TEARDOWN), 0, a.st, 45);
+    mbar_drain(bar(B_BK), 0, a.st, 46);
   }
   tc_fence_before();
   __syncthreads();

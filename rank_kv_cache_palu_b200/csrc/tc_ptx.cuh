@@ -276,6 +276,19 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo_bytes, ui
   return d;
 }
 
+// True on one lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Shared-memory descriptor `bytes` further on (a multiple of 16; shared memory ends below the 18 bits of
+// its address field): one addition where building a descriptor takes a dozen instructions.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  return (desc & 0xffffffff00000000ull) | ((uint32_t)desc + (bytes >> 4));
+}
+
 // Register budget of this warpgroup after a warp-specialised split.
 template <uint32_t N>
 __device__ __forceinline__ void setmaxnreg_dec() {
