@@ -3,8 +3,8 @@
 //
 // One CTA per (query, head): the list's main partial and its continuations (mostly one
 // or none: a CTA of the walk ends inside few lists), then a GEMV over B_v's r_v rows,
-// 64 output pairs × 4 interleaved row quarters, as in the dense combine.  Bound by the
-// L2 reads of B_v (32 KB per CTA at r_v = 128) and by latency.
+// 16 column groups of 16 bytes × 16 row lanes.  Bound by latency and, for many queries,
+// by the L2 reads of B_v (32 KB per CTA at r_v = 128).
 #include <math.h>
 
 #include "palu_common.cuh"
@@ -15,95 +15,110 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float2 load_pair(const T* p) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-  if constexpr (sizeof(T) == 2) {
-    const T* e = reinterpret_cast<const T*>(&w);
-    float2 r;
-    if constexpr (__is_same(T, __half)) r = make_float2(__half2float(e[0]), __half2float(e[1]));
-    else r = make_float2(__bfloat162float(e[0]), __bfloat162float(e[1]));
-    return r;
-  }
-}
+constexpr int kCols = 8;            // output columns of a thread: 16 bytes of a row of B_v
+constexpr int kMaxRv = 256;
+constexpr int kMaxHead = 128;
+constexpr int kRowLanes = kThreads / (kMaxHead / kCols);   // threads that share a column group, a row each in turn
 
-template <int ACT>
+// NR: rows of B_v per thread, r_v / kRowLanes.
+template <int ACT, int NR>
 __global__ void __launch_bounds__(kThreads) pages_combine_kernel(const __grid_constant__ DecodeArgs a) {
   using TA = typename Dt<ACT>::T;
-  extern __shared__ float smem[];
-  float* av = smem;               // [r_v]
-  float* red = av + a.r_v;        // [4][d_h] per-quarter outputs
+  constexpr int kRv = NR * kRowLanes;
+  __shared__ float av[kRv];
+  __shared__ float red[kThreads / 32][kMaxHead];
   const int hl = blockIdx.x, u = blockIdx.y, tid = threadIdx.x;
   const int gi = hl / a.gs, jh = hl % a.gs;
-  const int h = a.gm.g[gi] * a.gs + jh;   // model head
-  const int heads = a.gm.n * a.gs, stride = a.r_v + kPartHead;
-  const float* main_part = a.part + ((size_t)u * heads + hl) * stride;
+  const int g = a.gm.g[gi], h = g * a.gs + jh;   // model head
+  const int heads = a.gm.n * a.gs, stride = kRv + kPartHead;
   TA* out = reinterpret_cast<TA*>(a.out) + (size_t)u * a.o_bstride + (size_t)h * a.d_h;
   float* lse = a.lse != nullptr ? a.lse + (size_t)u * a.lse_bstride + h : nullptr;
 
-  int n = 0;                              // partials of the list
-  const float* cont = nullptr;
-  if (a.page_counts[(size_t)u * a.G + a.gm.g[gi]] > 0) {
-    const int2 seg = a.segments[(size_t)u * a.gm.n + gi];
-    n = 1 + seg.y;
-    cont = a.cont + ((size_t)seg.x * heads + hl) * stride;
+  // Everything whose address is known goes out at once: B_v, the list's count and segments, and its
+  // main partial (whatever it holds where the list is empty).
+  const int cg = tid % (kMaxHead / kCols), rl = tid / (kMaxHead / kCols);
+  const TA* Bv = reinterpret_cast<const TA*>(a.Bv) + (size_t)a.gm.v_row0[gi] * a.W + jh * a.d_h + cg * kCols;
+  uint4 b[NR];
+#pragma unroll
+  for (int k = 0; k < NR; ++k)
+    b[k] = cg * kCols < a.d_h ? __ldg(reinterpret_cast<const uint4*>(Bv + (size_t)(k * kRowLanes + rl) * a.W))
+                              : make_uint4(0, 0, 0, 0);
+  const float* main_part = a.part + ((size_t)u * heads + hl) * stride;
+  const int count = a.page_counts[(size_t)u * a.G + g];
+  const int2 seg = a.segments[(size_t)u * a.gm.n + gi];
+  float m0 = main_part[0], l0 = (main_part[1] + main_part[2]) + (main_part[3] + main_part[4]);
+  float v = tid < kRv ? main_part[kPartHead + tid] : 0.f;
+
+  float M = -INFINITY, L = 0.f;
+  if (count > 0) {
+    M = m0;
+    const float* cont = a.cont + ((size_t)seg.x * heads + hl) * stride;
+    const size_t step = (size_t)heads * stride;
+    for (int s = 0; s < seg.y; ++s) M = fmaxf(M, cont[s * step]);
+    if (M != -INFINITY) {
+      const float w0 = m0 == -INFINITY ? 0.f : expf(m0 - M);
+      L = w0 * l0;
+      v = m0 == -INFINITY ? 0.f : w0 * v;
+      for (int s = 0; s < seg.y; ++s) {
+        const float* p = cont + s * step;
+        if (p[0] == -INFINITY) continue;
+        const float w = expf(p[0] - M);
+        L += w * ((p[1] + p[2]) + (p[3] + p[4]));
+        if (tid < kRv) v = fmaf(w, p[kPartHead + tid], v);
+      }
+    }
   }
-  auto partial = [&](int s) { return s == 0 ? main_part : cont + (size_t)(s - 1) * heads * stride; };
-  float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, partial(s)[0]);
   if (M == -INFINITY) {
     for (int d = tid; d < a.d_h; d += kThreads) out[d] = Dt<ACT>::from_f(0.f);
     if (tid == 0 && lse != nullptr) *lse = -INFINITY;
     return;
   }
-  float L = 0.f;
-  for (int s = 0; s < n; ++s) {
-    const float* p = partial(s);
-    const float w = p[0] == -INFINITY ? 0.f : expf(p[0] - M);
-    L += w * ((p[1] + p[2]) + (p[3] + p[4]));
+  if (tid < kRv) av[tid] = v * (1.f / L);
+  __syncthreads();
+  float acc[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const float x = av[k * kRowLanes + rl];
+    const TA* e = reinterpret_cast<const TA*>(&b[k]);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(x, Dt<ACT>::to_f(e[c]), acc[c]);
   }
-  const float invL = 1.f / L;
-  for (int r = tid; r < a.r_v; r += kThreads) {
-    float v = 0.f;
-    for (int s = 0; s < n; ++s) {
-      const float* p = partial(s);
-      if (p[0] != -INFINITY) v = fmaf(expf(p[0] - M), p[kPartHead + r], v);
-    }
-    av[r] = v * invL;
+  // a warp holds two rows' lanes of every column group, the block eight warps
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], 16);
+  if ((tid & 31) < 16) {
+    float4* r = reinterpret_cast<float4*>(&red[tid >> 5][cg * kCols]);
+    r[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    r[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   }
   __syncthreads();
-  const TA* Bv = reinterpret_cast<const TA*>(a.Bv) + (size_t)a.gm.v_row0[gi] * a.W + jh * a.d_h;
-  const int d0 = 2 * (tid & 63), rq = tid >> 6;
-  if (d0 < a.d_h) {
-    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-#pragma unroll 8
-    for (int r = rq; r < a.r_v; r += 8) {      // r_v is a multiple of 64
-      const float2 b0 = load_pair(Bv + (size_t)r * a.W + d0);
-      const float2 b1 = load_pair(Bv + (size_t)(r + 4) * a.W + d0);
-      acc0.x = fmaf(av[r], b0.x, acc0.x);
-      acc0.y = fmaf(av[r], b0.y, acc0.y);
-      acc1.x = fmaf(av[r + 4], b1.x, acc1.x);
-      acc1.y = fmaf(av[r + 4], b1.y, acc1.y);
-    }
-    red[rq * a.d_h + d0] = acc0.x + acc1.x;
-    red[rq * a.d_h + d0 + 1] = acc0.y + acc1.y;
+  for (int d = tid; d < a.d_h; d += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += red[w][d];
+    out[d] = Dt<ACT>::from_f(s);
   }
-  __syncthreads();
-  for (int d = tid; d < a.d_h; d += kThreads)
-    out[d] = Dt<ACT>::from_f((red[d] + red[a.d_h + d]) + (red[2 * a.d_h + d] + red[3 * a.d_h + d]));
   if (tid == 0 && lse != nullptr) *lse = M + logf(L);
+}
+
+template <int ACT>
+cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
+  const dim3 grid(a.gm.n * a.gs, a.batch);
+  if (a.r_v == 128) pages_combine_kernel<ACT, 128 / kRowLanes><<<grid, kThreads, 0, st>>>(a);
+  else if (a.r_v == kMaxRv) pages_combine_kernel<ACT, kMaxRv / kRowLanes><<<grid, kThreads, 0, st>>>(a);
+  else return cudaErrorInvalidValue;
+  count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_pages_combine(const DecodeArgs& a, cudaStream_t st) {
-  const size_t smem = sizeof(float) * (a.r_v + 4 * a.d_h);
-  const dim3 grid(a.gm.n * a.gs, a.batch);
-  if (a.act == PALU_F16) pages_combine_kernel<PALU_F16><<<grid, kThreads, smem, st>>>(a);
-  else if (a.act == PALU_BF16) pages_combine_kernel<PALU_BF16><<<grid, kThreads, smem, st>>>(a);
-  else return cudaErrorInvalidValue;
-  count_launch();
-  return cudaGetLastError();
+  if (a.act == PALU_F16) return launch<PALU_F16>(a, st);
+  if (a.act == PALU_BF16) return launch<PALU_BF16>(a, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace palu
