@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nkc = r_k / kChunk;
   const uint32_t qt_bytes = (uint32_t)nkc * kN * 128;    // of one buffer
 
+  start_next();      // the merge; its CTAs find room as this launch's leave
   if (threadIdx.x == 0) {
     abort_init(abort_flag, a.wait_cycles);
     for (int i = 0; i < kNZK; ++i) {
@@ -180,20 +181,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
+      // the folded query of the segment that tile k begins: rows 0-7 of each chunk's 16
+      auto push_q = [&](int k) -> bool {
+        ++seg;
+        const int qb = seg % kNQ;
+        if (!mbar_wait(bar(F_QT_EMPTY + qb), ((seg / kNQ) & 1) ^ 1, abort_flag, st, 12)) return false;
+        mbar_expect_tx(bar(F_QT_FULL + qb), (uint32_t)nkc * 1024);
+        const uint8_t* src = static_cast<const uint8_t*>(qt) +
+                             ((size_t)tiles[k].unit * gm.n + gi) * 2 * kMaxG * a.r_k * 2;   // units 16·a.r_k bytes apart
+        for (int c = 0; c < nkc; ++c)
+          bulk_load(base + L.qt + qb * qt_bytes + c * kN * 128, src + (size_t)c * 1024, 1024, bar(F_QT_FULL + qb));
+        ++q_issued;
+        return true;
+      };
       bool ok = true;
       for (int k = 0; k < N && ok && !*abort_flag; ++k) {
-        if (tiles[k].info & kTileFirst) {
-          // the segment's folded query: rows 0-7 of each chunk's 16
-          ++seg;
-          const int qb = seg % kNQ;
-          if (!mbar_wait(bar(F_QT_EMPTY + qb), ((seg / kNQ) & 1) ^ 1, abort_flag, st, 12)) break;
-          mbar_expect_tx(bar(F_QT_FULL + qb), (uint32_t)nkc * 1024);
-          const uint8_t* src = static_cast<const uint8_t*>(qt) +
-                               ((size_t)tiles[k].unit * gm.n + gi) * 2 * kMaxG * a.r_k * 2;   // units 16·a.r_k bytes apart
-          for (int c = 0; c < nkc; ++c)
-            bulk_load(base + L.qt + qb * qt_bytes + c * kN * 128, src + (size_t)c * 1024, 1024, bar(F_QT_FULL + qb));
-          ++q_issued;
-        }
+        if (k > 0 && (tiles[k].info & kTileFirst) && !push_q(k)) break;
         const uint8_t* src = gm.zk[gi] + (size_t)max(tiles[k].page, 0) * gm.k_page;
         for (int c = 0; c < nkc; ++c) {
           if (!mbar_wait(bar(F_ZK_EMPTY + zs), zph ^ 1, abort_flag, st, 10)) { ok = false; break; }
@@ -202,9 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++zk_issued;
           if (++zs == kNZK) { zs = 0; zph ^= 1; }
         }
+        if (k == 0) {
+          await_previous();      // the query fold; the first tile's latents are on their way meanwhile
+          ok = ok && push_q(0);
+        }
         if (ok && k >= 1) ok = push_zv(k - 1);
       }
       if (ok && N >= 1 && !*abort_flag) push_zv(N - 1);
+      await_previous();   // with no tile too: no launch of the step ends before the one it follows
       // after an abort, copies already issued still land in shared memory: wait for them
       drain_ring(bar(F_ZK_FULL), kNZK, zk_issued, st, 10);
       drain_ring(bar(F_ZV_FULL), kNZV, zv_issued, st, 11);
@@ -428,9 +436,16 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   auto kern = decode_pages_fused_kernel<ACT, NRV>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(a.walk_ctas, a.gm.n), kThreads, smem, st>>>(a, a.fused_q);
+  cudaLaunchAttribute at = dependent_launch();
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(a.walk_ctas, a.gm.n);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
   count_launch();
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&c, kern, a, (const void*)a.fused_q);
 }
 
 }  // namespace

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
   const uint32_t k_blk_bytes = (uint32_t)a.P * (kInt4 ? r_k / 2 : 2 * r_k);   // this entry's block of a page
   const Tile* tiles = reinterpret_cast<const Tile*>(sbase + L.tiles);
 
+  start_next();      // the merge; its CTAs find room as this launch's leave
   // ---------------------------------------------------------------- setup
   if (threadIdx.x == 0) {
     abort_init(abort_flag, a.wait_cycles);

@@ -24,6 +24,7 @@ constexpr int kFoldSeqs = 4;
 template <int ACT, bool IMAGE>
 __global__ void __launch_bounds__(256) fold_query_kernel(const __grid_constant__ DecodeArgs a, int qslots, void* qt) {
   using TA = typename Dt<ACT>::T;
+  if constexpr (IMAGE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the walk lays out its tiles
   // rows padded by 4 floats: the four heads' 16-byte reads of one warp land in distinct banks
   __shared__ __align__(16) float qs[kFoldSeqs][kMaxG][128 + 4];
   // blockIdx.x: entry gi of the group map (model group g)

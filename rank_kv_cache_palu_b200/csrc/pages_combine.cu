@@ -9,6 +9,7 @@
 
 #include "palu_common.cuh"
 #include "palu_internal.h"
+#include "pages_walk.cuh"
 
 namespace palu {
 namespace {
@@ -34,8 +35,8 @@ __global__ void __launch_bounds__(kThreads) pages_combine_kernel(const __grid_co
   TA* out = reinterpret_cast<TA*>(a.out) + (size_t)u * a.o_bstride + (size_t)h * a.d_h;
   float* lse = a.lse != nullptr ? a.lse + (size_t)u * a.lse_bstride + h : nullptr;
 
-  // Everything whose address is known goes out at once: B_v, the list's count and segments, and its
-  // main partial (whatever it holds where the list is empty).
+  // B_v and the list's count do not depend on the walk and are loaded while it ends; then the list's
+  // segments and its main partial (whatever it holds where the list is empty) together.
   const int cg = tid % (kMaxHead / kCols), rl = tid / (kMaxHead / kCols);
   const TA* Bv = reinterpret_cast<const TA*>(a.Bv) + (size_t)a.gm.v_row0[gi] * a.W + jh * a.d_h + cg * kCols;
   uint4 b[NR];
@@ -43,8 +44,9 @@ __global__ void __launch_bounds__(kThreads) pages_combine_kernel(const __grid_co
   for (int k = 0; k < NR; ++k)
     b[k] = cg * kCols < a.d_h ? __ldg(reinterpret_cast<const uint4*>(Bv + (size_t)(k * kRowLanes + rl) * a.W))
                               : make_uint4(0, 0, 0, 0);
-  const float* main_part = a.part + ((size_t)u * heads + hl) * stride;
   const int count = a.page_counts[(size_t)u * a.G + g];
+  await_previous();       // the walk: its segments and partials
+  const float* main_part = a.part + ((size_t)u * heads + hl) * stride;
   const int2 seg = a.segments[(size_t)u * a.gm.n + gi];
   float m0 = main_part[0], l0 = (main_part[1] + main_part[2]) + (main_part[3] + main_part[4]);
   float v = tid < kRv ? main_part[kPartHead + tid] : 0.f;
@@ -105,12 +107,17 @@ __global__ void __launch_bounds__(kThreads) pages_combine_kernel(const __grid_co
 
 template <int ACT>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t st) {
-  const dim3 grid(a.gm.n * a.gs, a.batch);
-  if (a.r_v == 128) pages_combine_kernel<ACT, 128 / kRowLanes><<<grid, kThreads, 0, st>>>(a);
-  else if (a.r_v == kMaxRv) pages_combine_kernel<ACT, kMaxRv / kRowLanes><<<grid, kThreads, 0, st>>>(a);
-  else return cudaErrorInvalidValue;
+  cudaLaunchAttribute at = dependent_launch();
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(a.gm.n * a.gs, a.batch);
+  c.blockDim = dim3(kThreads);
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
   count_launch();
-  return cudaGetLastError();
+  if (a.r_v == 128) return cudaLaunchKernelEx(&c, pages_combine_kernel<ACT, 128 / kRowLanes>, a);
+  if (a.r_v == kMaxRv) return cudaLaunchKernelEx(&c, pages_combine_kernel<ACT, kMaxRv / kRowLanes>, a);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -119,6 +119,20 @@ __device__ __forceinline__ int walk_tiles(const DecodeArgs& a, int g, int gi, bo
   return n;
 }
 
+// The kernels of a step follow one another as programmatic dependents: each lets the next one start
+// (start_next), which does what it can without this one's results, then waits for all of them
+// (await_previous; at once where the launch before was an ordinary one).
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch attribute of a programmatic dependent of the launch before it in the stream.
+inline cudaLaunchAttribute dependent_launch() {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return at;
+}
+
 // Partial of the segment that tile t ends, for head hl of the launch:
 // m, l of the four warps, then a[r_v] (float32).
 __device__ __forceinline__ float* segment_part(const DecodeArgs& a, const Tile& t, int hl) {
