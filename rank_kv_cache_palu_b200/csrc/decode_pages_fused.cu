@@ -13,7 +13,7 @@
 //   - the softmax weights reach the value MMA as hi + lo 16-bit numbers, rows p and
 //     4 + p of its 16, so that no weight is rounded to 16 bits.
 // Bound by the latents' bytes from HBM: 14 queries x 64 pages in each of 8 groups (r 256/128,
-// f16, 0.71 GB) 134 us with the fold and the combine, 0.81 of the measured copy bandwidth; this
+// f16, 0.71 GB) 126 us with the fold and the merge, 0.86 of the measured copy bandwidth; this
 // kernel alone 115 us, 0.94.
 #include <cuda.h>
 #include <math.h>

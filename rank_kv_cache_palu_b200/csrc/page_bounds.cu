@@ -22,7 +22,7 @@
 // (2·128·r_k·W flops per page and group), by the B_k load and one page's latency
 // at a decode step's one page per sequence.  Measured in the 7B shape (8 groups of 4
 // heads, r_k 256, bf16): 64 pages 18.9 us (0.91 PFLOP/s with the start-up; 8 tiles a CTA
-// of ~2.2k cycles, 2.05k of them MMA), one page of each of 16 sequences 9.5 us.
+// of ~2.2k cycles, 2.05k of them MMA), one page of each of 16 sequences 9.7 us.
 //
 // Every other shape, and float32, takes the CUDA-core kernel, bound by its FMAs and, for
 // a page or two, by latency (two float32 heads of 64, r_k 64, 2 pages: 18 us).
