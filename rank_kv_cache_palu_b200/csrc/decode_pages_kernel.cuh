@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
     // ============================================================ int4 key codes (warps 12-15)
     // Chunk c of a tile = entries [64c, 64c + 64) of all 128 tokens, i.e. scale
     // blocks 2c and 2c+1 = 16-byte units 2c and 2c+1 of each token's row of codes.
-    // Thread t takes both units of token t, loaded straight into registers three
+    // Thread t takes both units of token t, loaded straight into registers two
     // chunks ahead of the conversion, while later pages are pulled into L2.  Entries
     // are written PAIRED (K position p of the operand holds entry paired_row(p)), which
     // saves byte permutes; B_k's rows are loaded in the same order, so the key MMA sums
@@ -169,54 +169,51 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       prefetch_l2(gm.zv[gi] + (size_t)ppg * gm.v_page, (uint32_t)(a.P * a.v_row));
       prefetch_l2(gm.zvs[gi] + (size_t)ppg * gm.vs_page, (uint32_t)(a.P * a.vs_row));
     };
+    // The issue slots of the SM are what this kernel runs out of, so addresses take few of them: unit u
+    // of a token's 128-byte row lies at (row + 16 (t mod 8)) XOR 16 u, in a page as in a ring stage
+    // (rows start on 128 bytes), and a page's pointers are made once per tile.
+    const uint32_t row0 = (uint32_t)t * 128 + ((uint32_t)(t & 7) << 4);
+    const uint8_t* codes = nullptr;
+    const uint8_t* scales = nullptr;
     auto issue = [&](int n, Slot& sl) {
       if (n >= NC) return;
-      const int pg = max(tiles[n >> 2].page, 0);   // of a bad page (reported): any page's, the result is void
-      const uint8_t* row = gm.zk[gi] + (size_t)pg * gm.k_page + t * 128;
-      const uint8_t* srow = gm.zks[gi] + (size_t)pg * gm.ks_page + (size_t)t * a.ks_row;
+      const int c = n & 3;
+      if (c == 0) {
+        const size_t pg = (size_t)max(tiles[n >> 2].page, 0);   // of a bad page (reported): any page's, the result is void
+        codes = gm.zk[gi] + pg * gm.k_page;
+        scales = gm.zks[gi] + pg * gm.ks_page + (size_t)t * a.ks_row;
+      }
 #pragma unroll
       for (int ub = 0; ub < 2; ++ub) {
-        const int u = 2 * (n & 3) + ub;
-        sl.raw[ub] = __ldg(reinterpret_cast<const uint4*>(row + ((u ^ (t & 7)) << 4)));
-        sl.sc[ub] = __ldg(reinterpret_cast<const unsigned short*>(srow + 2 * u));
+        sl.raw[ub] = __ldg(reinterpret_cast<const uint4*>(codes + (row0 ^ (uint32_t)(32 * c + 16 * ub))));
+        sl.sc[ub] = __ldg(reinterpret_cast<const unsigned short*>(scales + 4 * c + 2 * ub));
       }
     };
     int stage = 0;
     uint32_t phase = 0;
-    auto consume = [&](int n, const Slot& sl) -> bool {
-      if (n >= NC) return true;
-      if (!mbar_wait(bar(BAR_ZK_EMPTY + stage), phase ^ 1, abort_flag, st, 12)) return false;
-      const uint32_t dst = base + L.zk + stage * kZkBytes + t * 128;
+    Slot s0, s1;                                       // chunks n and n + 1
+    for (int kk = 1; kk <= kPrefetch; ++kk) prefetch_tile(kk);
+    issue(0, s0);
+    issue(1, s1);
+    // One load batch and one conversion per chunk: a single copy of the conversion
+    // code keeps the kernel's instruction footprint small.  A slot is copied an iteration after
+    // its loads went out (copied at once it would wait for them).
+#pragma unroll 1
+    for (int n = 0; n < NC; ++n) {
+      if (!mbar_wait(bar(BAR_ZK_EMPTY + stage), phase ^ 1, abort_flag, st, 12)) break;
+      const uint32_t dst = base + L.zk + stage * kZkBytes + row0;
 #pragma unroll
       for (int ub = 0; ub < 2; ++ub) {
-        const uint32_t w[4] = {sl.raw[ub].x, sl.raw[ub].y, sl.raw[ub].z, sl.raw[ub].w};
+        const uint32_t w[4] = {s0.raw[ub].x, s0.raw[ub].y, s0.raw[ub].z, s0.raw[ub].w};
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          st_shared_v4(dst + (((4 * ub + m) ^ (t & 7)) << 4), dequant8<ACT, true>(w[m], sl.sc[ub]));
+        for (int m = 0; m < 4; ++m) st_shared_v4(dst ^ (uint32_t)(64 * ub + 16 * m), dequant8<ACT, true>(w[m], s0.sc[ub]));
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_ZK_FULL + stage));
       if (++stage == kNZK) { stage = 0; phase ^= 1; }
-      return true;
-    };
-    Slot s0, s1, s2, s3;                               // after the shift: chunks n, n+1, n+2; s3 takes n+3
-    for (int kk = 1; kk <= kPrefetch; ++kk) prefetch_tile(kk);
-    issue(0, s1);
-    issue(1, s2);
-    issue(2, s3);
-    // One load batch and one conversion per chunk: a single copy of the conversion
-    // code keeps the kernel's instruction footprint small.  The register slots shift
-    // down at the top of each iteration, before the next loads are issued, so a shift
-    // never copies a slot whose loads went out in the same iteration (the copy would
-    // wait for them).
-#pragma unroll 1
-    for (int n = 0; n < NC && !*abort_flag; ++n) {
       s0 = s1;
-      s1 = s2;
-      s2 = s3;
-      issue(n + 3, s3);
-      if (!consume(n, s0)) break;
+      issue(n + 2, s1);
       if ((n & 3) == 0) prefetch_tile((n >> 2) + 1 + kPrefetch);
     }
   } else if (warp >= 4) {
@@ -553,62 +550,66 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         uint4 raw[3];
         uint16_t sc[3];
       };
+      // item j of this thread: offsets of its unit in a page (stage 0 of the tile: unit i / 64 of token
+      // i mod 64) and in a ring stage, of its scale in the page's scales
+      uint32_t from[3], to[3], sfrom[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const uint32_t i = vt + 96 * j, t = i & 63, u = i >> 6;
+        from[j] = t * 128 + ((u ^ (t & 7)) << 4);
+        to[j] = (i >> 7) * (kZvBytes / 2) + t * 128 + (((4 * (u & 1)) ^ (t & 7)) << 4);
+        sfrom[j] = t * (uint32_t)a.vs_row + 2 * u;
+      }
+      const int last = vt + 192 < 256 ? 3 : 2;           // items of this thread
+      const uint8_t* codes = nullptr;
+      const uint8_t* scales = nullptr;
+      int rows = 0;
       // stage s of tile k (k >= N: nothing)
       auto issue = [&](int k, int s, Slot& sl) {
         if (k >= N) return;
-        const int pg = max(tiles[k].page, 0);
-        const uint8_t* blk = gm.zv[gi] + (size_t)pg * gm.v_page;
-        const uint8_t* sblk = gm.zvs[gi] + (size_t)pg * gm.vs_page;
-        const int mb = s >> 1, th = s & 1, rows = tile_rows(tiles[k].info);
-  #pragma unroll
+        if (s == 0) {
+          const size_t pg = (size_t)max(tiles[k].page, 0);
+          codes = gm.zv[gi] + pg * gm.v_page;
+          scales = gm.zvs[gi] + pg * gm.vs_page;
+          rows = tile_rows(tiles[k].info);
+        }
+        const uint32_t mb = s >> 1, th = s & 1;
+        const uint32_t srow = th * 64 * (uint32_t)a.vs_row + 8 * mb;
+#pragma unroll
         for (int j = 0; j < 3; ++j) {
-          const int i = vt + 96 * j;
-          if (i < 256) {
-            const int t = 64 * th + (i & 63), u = 4 * mb + (i >> 6);
-            // rows past the sequence become zeros, whatever the page holds there
-            sl.raw[j] = make_uint4(0u, 0u, 0u, 0u);
-            sl.sc[j] = 0;
-            if (t < rows) {
-              sl.raw[j] = __ldg(reinterpret_cast<const uint4*>(blk + t * 128 + ((u ^ (t & 7)) << 4)));
-              sl.sc[j] = __ldg(reinterpret_cast<const unsigned short*>(sblk + (size_t)t * a.vs_row + 2 * u));
-            }
+          // rows past the sequence become zeros, whatever the page holds there
+          sl.raw[j] = make_uint4(0u, 0u, 0u, 0u);
+          sl.sc[j] = 0;
+          if (j < last && (int)(64 * th) + ((vt + 96 * j) & 63) < rows) {
+            sl.raw[j] = __ldg(reinterpret_cast<const uint4*>(codes + (from[j] ^ (64 * mb)) + th * 8192));
+            sl.sc[j] = __ldg(reinterpret_cast<const unsigned short*>(scales + sfrom[j] + srow));
           }
         }
       };
       int stage = 0;
       uint32_t phase = 0;
-      auto consume = [&](const Slot& sl) -> bool {
-        if (!mbar_wait(bar(BAR_ZV_EMPTY + stage), phase ^ 1, abort_flag, st, 13)) return false;
+      Slot s0, s1;                                       // this stage and the next
+      issue(0, 0, s0);
+      issue(0, 1, s1);
+#pragma unroll 1
+      for (int n = 0; n < N * kSPT; ++n) {
+        if (!mbar_wait(bar(BAR_ZV_EMPTY + stage), phase ^ 1, abort_flag, st, 13)) break;
         const uint32_t dst = base + L.zv + stage * kZvBytes;
-  #pragma unroll
+#pragma unroll
         for (int j = 0; j < 3; ++j) {
-          const int i = vt + 96 * j;
-          if (i < 256) {
-            const int tr64 = i & 63, blk = (i >> 7), ub = (i >> 6) & 1;   // token row, entry block, unit
-            const uint32_t w[4] = {sl.raw[j].x, sl.raw[j].y, sl.raw[j].z, sl.raw[j].w};
-            const uint32_t row = dst + blk * (kZvBytes / 2) + tr64 * 128;
-  #pragma unroll
+          if (j < last) {
+            const uint32_t w[4] = {s0.raw[j].x, s0.raw[j].y, s0.raw[j].z, s0.raw[j].w};
+#pragma unroll
             for (int m = 0; m < 4; ++m)
-              st_shared_v4(row + (((4 * ub + m) ^ (tr64 & 7)) << 4), dequant8<ACT, true>(w[m], sl.sc[j]));
+              st_shared_v4((dst + to[j]) ^ (uint32_t)(16 * m), dequant8<ACT, true>(w[m], s0.sc[j]));
           }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(BAR_ZV_FULL + stage));
         if (++stage == kNVS) { stage = 0; phase ^= 1; }
-        return true;
-      };
-      // the next stage to load is two ahead of the conversion
-      Slot s0, s1, s2;                                   // after the shift: this stage, the next; s2 takes the one after
-      issue(0, 0, s1);
-      issue(0, 1, s2);
-      // as for the keys: the slots shift before the next loads go out
-  #pragma unroll 1
-      for (int n = 0; n < N * kSPT && !*abort_flag; ++n) {
         s0 = s1;
-        s1 = s2;
-        issue((n + 2) / kSPT, (n + 2) % kSPT, s2);
-        if (!consume(s0)) break;
+        issue((n + 2) / kSPT, (n + 2) % kSPT, s1);
       }
     } else if (warp == 0) {
       // ============================================================ z_k producer (bulk copies)
