@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
     const uint8_t* scales = nullptr;
     // Loads past the last chunk repeat the last tile's: a condition on them would let the slot take its
     // values through other registers, at the end of the iteration, when they have not come yet
-    // (650 cycles a chunk; 239 -> @ us in all).
+    // (32 queries x 16 pages: 234 us so, 230 without).
     auto issue = [&](int n, Slot& sl) {
       const int c = n & 3;
       if (c == 0 && n < NC) {
