@@ -21,7 +21,7 @@
 // Measured in the 7B shape, r 256/128 bf16, 16 queries x 32 pages in each of 8 groups: 138 to 144 us
 // with the merge (0.96 PFLOP/s of key and value products or more, 0.58 of the burst peak), bound as the dense kernel by
 // the coupling of the operand rings to the TMEM slots; one query x 16 pages 17.6 us.  int4, r 256/256, 8 sequences x 4 queries x
-// 16 pages: 239 us, bound by the conversion of codes.
+// 16 pages: 230 us, bound by the conversion of codes.
 #pragma once
 
 #include "decode_tc_kernel.cuh"
