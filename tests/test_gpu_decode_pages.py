@@ -257,3 +257,52 @@ def test_timeout_reports_and_recovers(name):
     finally:
         P.palu_debug_timeout_test()
     compare(case, *run(case, pools, q, q_pos, lists, 3), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["int4_f16", "int4_bf16"])
+def test_scales_behind_the_last_token_are_not_read(name):
+    case = make_decode_case(CASES[name][0], [133, 7])
+    q, q_pos = queries(case, 1)
+    pools = build_pools(case)
+    w = case.w
+    for pool in ("zks", "zvs"):
+        raw = pools[pool].view(torch.float16).view(case.num_pages, w.groups, w.page_size, -1)
+        for i, t in enumerate(case.seq_lens):
+            page, rest = int(case.page_table[i, t // w.page_size]), raw[:, :, t % w.page_size:]
+            rest[page, :, 0::2], rest[page, :, 1::2] = float("nan"), float("inf")
+    lists = [[[[0, 1]] * w.groups], [[[0]] * w.groups]]
+    compare(case, *run(case, pools, q, q_pos, lists, 2), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16", "tiny_f32"])
+def test_calls_that_follow_at_once_share_a_workspace(name):
+    """Calls of other sizes behind one another on a stream, nothing waited for: each as on its own."""
+    case = make_decode_case(CASES[name][0], [900, 0, 1, 400])
+    pools, cfg, w = build_pools(case), case.cfg, case.w
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    table, lens = dev(case.page_table), torch.tensor(case.seq_lens, dtype=torch.int32, device="cuda")
+    Bk, Bv = case.B_k.cuda(), case.B_v.cuda()
+    ws = torch.zeros(P.palu_decode_pages_workspace_size(cfg, 4, 4, 7), dtype=torch.uint8, device="cuda")
+    calls = []
+    for n in range(12):
+        Q, keep = (1, 4, 2)[n % 3], (7, 1, 3)[n % 3]
+        q, q_pos = queries(case, Q, seed=n)
+        lists = pick_lists(case, Q, keep, seed=n)
+        if n % 4 == 3:
+            lists = [[[[]] * w.groups for _ in range(Q)] for _ in lists]     # nothing listed at all
+        flat = np.full((4, Q, w.groups, keep), -1, np.int32)
+        counts = np.zeros((4, Q, w.groups), np.int32)
+        for i, j, g in np.ndindex(4, Q, w.groups):
+            flat[i, j, g, :len(lists[i][j][g])] = lists[i][j][g]
+            counts[i, j, g] = len(lists[i][j][g])
+        out = torch.full((4, Q, w.num_heads, w.head_dim), 9.0, dtype=TORCH_DTYPE[w.act_dtype], device="cuda")
+        lse = torch.full((4, Q, w.num_heads), 9.0, device="cuda")
+        calls.append((q, q_pos, lists, q.cuda(), dev(q_pos), dev(flat), dev(counts), out, lse))
+    torch.cuda.synchronize()
+    for _, _, _, q, q_pos, flat, counts, out, lse in calls:
+        P.palu_decode_attn_pages(cfg, q, q_pos, pools["zk"], pools["zv"], pools["zks"], pools["zvs"], pools["pos"], table,
+                                 lens, flat, counts, case.num_pages, Bk, Bv, out, lse, ws)
+    torch.cuda.synchronize()
+    assert P.palu_get_device_status(ws)[0] == 0
+    for q, q_pos, lists, *_, out, lse in calls:
+        compare(case, out.double().cpu().numpy(), lse.double().cpu().numpy(), q, q_pos, lists, uniform(case))
