@@ -168,3 +168,45 @@ def test_another_stream():
     s.wait_stream(torch.cuda.current_stream())
     p.call(new, stream=s)
     p.check(S.plan_append(8, [1] * 30, lens, table, stack, free, 30))
+
+
+def test_many_short_sequences():
+    """Rows of one thread belong to several sequences, empty ones between them."""
+    rng = random.Random(11)
+    batch, wide = 8192, 4
+    new = [rng.choice([0, 0, 0, 1, 1, 2, 3, 40]) for _ in range(batch // 2)] + [rng.choice([0, 30]) for _ in range(batch // 2)]
+    assert sum(new) > 148 * 512
+    run_case(rng, batch, 16, wide, batch * wide, new, None, fill=0.3)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_outputs_that_start_anywhere(offset):
+    rng = random.Random(12)
+    lens, table, stack, had = make_state(rng, 5, 24, 2000, 10000, 0.2)
+    new = [19999, 0, 30001, 17, 40000]
+    n = sum(new) + 6
+    p = Plan(24, lens, table, stack, had, n)
+    p.slots, p.positions = (torch.full((n + 4,), 77, dtype=torch.int32, device="cuda")[offset:offset + n] for _ in range(2))
+    p.call(torch.tensor(new, dtype=torch.int32, device="cuda"))
+    p.check(S.plan_append(24, new, lens, table, stack, had, n))
+
+
+@pytest.mark.parametrize("page,wide", [(1000000, 2147), (524296, 4096), (524296, 4095), (8, 3000), (40, 3000), (1 << 20, 2047)])
+def test_quotients_by_any_page_size(page, wide):
+    """Positions up to the last below 2^31 that the page size allows."""
+    cap = page * wide
+    if cap >= 2 ** 31:                                # 524296·4096 = 2^31 + 32768: past the documented limit
+        p = Plan(page, [0], [[-1] * wide], list(range(wide)), wide, 1)
+        with pytest.raises(P.PaluError):
+            p.call(torch.ones(1, dtype=torch.int32, device="cuda"))
+        return
+    for length, new in ((cap - 90001, 90001), (cap - 7 * page // 3, 300), (page - 1, 2), (0, 1)):
+        had = -(-length // page)
+        table = [list(range(had)) + [-1] * (wide - had)]
+        stack = list(range(wide - 1, had - 1, -1)) + [-1] * had
+        n = min(new, cap - length)
+        if length < 0:
+            continue
+        p = Plan(page, [length], table, stack, wide - had, n)
+        p.call(torch.tensor([n], dtype=torch.int32, device="cuda"))
+        p.check(S.plan_append(page, [n], [length], table, stack, wide - had, n))
