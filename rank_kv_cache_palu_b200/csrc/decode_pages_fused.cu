@@ -194,21 +194,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++q_issued;
         return true;
       };
+      // The first tile's latents go out ahead of its query, which waits for the fold: as many chunks as
+      // the ring holds, for a further one waits for an MMA, and the MMAs wait for the query.
+      auto first_query = [&]() -> bool {
+        await_previous();
+        return push_q(0);
+      };
       bool ok = true;
       for (int k = 0; k < N && ok && !*abort_flag; ++k) {
         if (k > 0 && (tiles[k].info & kTileFirst) && !push_q(k)) break;
         const uint8_t* src = gm.zk[gi] + (size_t)max(tiles[k].page, 0) * gm.k_page;
         for (int c = 0; c < nkc; ++c) {
+          if (k == 0 && c == kNZK && !first_query()) { ok = false; break; }
           if (!mbar_wait(bar(F_ZK_EMPTY + zs), zph ^ 1, abort_flag, st, 10)) { ok = false; break; }
           mbar_expect_tx(bar(F_ZK_FULL + zs), kStageBytes);
           bulk_load(base + L.zk + zs * kStageBytes, src + (size_t)c * kStageBytes, kStageBytes, bar(F_ZK_FULL + zs));
           ++zk_issued;
           if (++zs == kNZK) { zs = 0; zph ^= 1; }
         }
-        if (k == 0) {
-          await_previous();      // the query fold; the first tile's latents are on their way meanwhile
-          ok = ok && push_q(0);
-        }
+        if (k == 0 && nkc <= kNZK) ok = ok && first_query();
         if (ok && k >= 1) ok = push_zv(k - 1);
       }
       if (ok && N >= 1 && !*abort_flag) push_zv(N - 1);

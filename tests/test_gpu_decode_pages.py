@@ -306,3 +306,35 @@ def test_calls_that_follow_at_once_share_a_workspace(name):
     assert P.palu_get_device_status(ws)[0] == 0
     for q, q_pos, lists, *_, out, lse in calls:
         compare(case, out.double().cpu().numpy(), lse.double().cpu().numpy(), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("Q", [1, 2])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("rank_k", [64, 320, 384, 448, 512])
+def test_norope_at_every_number_of_key_chunks(rank_k, act, Q):
+    """A list's first tile has more latent chunks than the ring has stages from key rank 448 on."""
+    w = w7b(rope_base=0.0, rank_k=rank_k, act_dtype=act, latent_dtype=act)
+    case = make_decode_case(w, [300, 0, 1, 900])
+    assert P.palu_decode_kernel_kind(case.cfg) == 3
+    q, q_pos = queries(case, Q)
+    lists = pick_lists(case, Q, 5, seed=rank_k)
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 5), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("ranks_k", [[128, 512], [448, 64]])
+def test_norope_ranks_per_group_up_to_the_largest(ranks_k):
+    case = make_ranked_case(w7b(rope_base=0.0), ranks_k, [128, 128], [300, 700], nq=2)
+    lists = [[[[0, 2], [1]], [[0], [0, 2]]], [[[5], [0, 3, 5]], [[1, 2], [4]]]]
+    out, lse = run(case, build_ranked_pools(case), case.q, case.q_pos, lists, 3, ranks=(ranks_k, [128, 128]))
+    w = case.w
+    for i in range(2):
+        zk, zv, Bk, Bv = case.oracle_inputs(i)
+        for j in range(2):
+            for g in range(2):
+                hs = slice(g * 4, g * 4 + 4)
+                ref, rl, size = S.decode_attention_pages(case.q[i, j, hs].double().numpy(), case.q_pos[i, j], zk[g][None],
+                                                         zv[g][None], case.positions(i), Bk[g][None], Bv[g][None], 4,
+                                                         w.rope_base, [lists[i][j][g]], w.page_size, True)
+                off = np.abs(out[i, j, hs] - ref)
+                assert (off <= HALF_STEP[w.act_dtype] * np.abs(ref) + SUM[w.act_dtype] * size).all()
+                np.testing.assert_allclose(lse[i, j, hs], rl, rtol=0, atol=LSE[w.act_dtype])
