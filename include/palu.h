@@ -447,11 +447,10 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
  * be finite on the tensor-core kernels.
  * A list that is not ascending or names a page past the sequence is reported as
  * PALU_ERR_DEVICE_BOUNDS (the result is void).  The softmax weights reach the
- * value product as the sum of two 16-bit numbers, so F16 / BF16 results carry
- * float32 accuracy up to the final rounding.  num_splits (0 = automatic) splits
- * the lists of the CUDA-core kernel; the tensor-core kernels deal all listed pages
- * of a head group out in equal shares and take any value.  ranks_k / ranks_v as in
- * the ranked calls.
+ * value product as the sum of three 16-bit numbers, as exact as in float32.
+ * num_splits (0 = automatic) splits the lists of the CUDA-core kernel; the
+ * tensor-core kernels deal all listed pages of a head group out in equal shares and
+ * take any value.  ranks_k / ranks_v as in the ranked calls.
  * batch·num_queries <= 65535, list_len <= 2^24 (PALU_ERR_UNSUPPORTED above). */
 palu_status palu_decode_pages_workspace_size(const palu_config* cfg, const int32_t* ranks_k,
                                              const int32_t* ranks_v, int batch, int num_queries, int list_len,

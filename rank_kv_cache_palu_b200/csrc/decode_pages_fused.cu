@@ -10,8 +10,8 @@
 //     a third of the time starting up;
 //   - the folded queries change with the segment: the producer brings each segment's
 //     (a 128-byte-swizzled image, fold_query.cuh) into one of three buffers;
-//   - the softmax weights reach the value MMA as hi + lo 16-bit numbers, rows p and
-//     4 + p of its 16, so that no weight is rounded to 16 bits.
+//   - the softmax weights reach the value MMA as sums of three 16-bit numbers
+//     (split_weight), rows p, 4 + p and 8 + p of its 16.
 // Bound by the latents' bytes from HBM: 14 queries x 64 pages in each of 8 groups (r 256/128,
 // f16, 0.71 GB) 126 us with the fold and the merge, 0.86 of the measured copy bandwidth; this
 // kernel alone 115 us, 0.94.
@@ -36,7 +36,8 @@ constexpr int kNZV = 4;             // z_v ring stages (pairs of column blocks)
 constexpr int kNQ = 3;              // folded-query buffers
 constexpr int kStageBytes = kTile * kChunk * 2;   // 16 KB: one column block of a page
 constexpr int kN = 16;              // score MMA columns: q̃ hi rows 0-3, lo rows 4-7, 8 padding rows
-constexpr int kNP = 16;             // value MMA columns: P hi rows 0-3, lo rows 4-7, padding
+constexpr int kNP = 16;             // value MMA columns: the weights' terms, heads in rows 0-3, 4-7, 8-11, padding
+static_assert(kWeightTerms * kMaxG <= kNP, "a row for each term of each head's weights");
 constexpr int kPBytes = kNP * kTile * 2;
 constexpr int kTmemCols = 128;      // 2 score slots × kN, 2 value buffers × r_v / 128 × kNP
 constexpr int kAt = 2 * kN;         // first value column
@@ -78,16 +79,6 @@ __host__ __device__ inline FusedSmem fused_smem(int r_k) {
   s.qt = o;   o += kNQ * (uint32_t)(r_k / kChunk) * kN * 128;   // [buffer][K chunk][16 rows][128 B]
   s.total = o;
   return s;
-}
-
-template <int ACT>
-__device__ __forceinline__ uint16_t to_bits(float v) {
-  const auto h = Dt<ACT>::from_f(v);
-  return *reinterpret_cast<const uint16_t*>(&h);
-}
-template <int ACT>
-__device__ __forceinline__ float from_bits(uint16_t u) {
-  return Dt<ACT>::to_f(*reinterpret_cast<const typename Dt<ACT>::T*>(&u));
 }
 
 // P tile, K-major with the 128-byte swizzle: row n, token k; tokens 0-63 and
@@ -335,11 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int mb = 0; mb < NRV; ++mb) {
-        float v[2 * kMaxG];                  // sums of the hi parts of P, then of the lo parts
-        tmem_ld8(tmem + lane_addr + kAt + (uint32_t)vb * NRV * kNP + mb * kNP, v);
+        float v[kNP];                        // sums of the weights' first terms, of the second, of the third
+        tmem_ld16(tmem + lane_addr + kAt + (uint32_t)vb * NRV * kNP + mb * kNP, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int p = 0; p < kMaxG; ++p) acc[mb][p] = fmaf(acc[mb][p], prev_scale[p], v[p] + v[kMaxG + p]);
+        for (int p = 0; p < kMaxG; ++p)
+          acc[mb][p] = fmaf(acc[mb][p], prev_scale[p], v[p] + (v[kMaxG + p] + v[2 * kMaxG + p]));
       }
       tc_fence_before();
       __syncwarp();
@@ -359,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row == 0) out[0] = m_run[p] * kLn2;
         if (lane == 0) out[1 + q4] = l;
 #pragma unroll
-        for (int mb = 0; mb < NRV; ++mb) out[kPartHead + mb * 128 + row] = acc[mb][p];
+        for (int mb = 0; mb < NRV; ++mb) out[kPartHead + mb * 128 + row] = acc[mb][p] * (1.f / kWeightScale<ACT>);
       }
       restart();
     };
@@ -405,9 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = fmaxf(m_run[p], mt);
         const float scale = m_new == -INFINITY ? 1.f : exp2f(m_run[p] - m_new);   // 1 while all masked
         const float pf = sc[p] != -INFINITY ? exp2f(sc[p] - m_new) : 0.f;
-        const uint16_t pb = to_bits<ACT>(pf);
-        *reinterpret_cast<uint16_t*>(pbuf + p_offset(p, row)) = pb;
-        *reinterpret_cast<uint16_t*>(pbuf + p_offset(kMaxG + p, row)) = to_bits<ACT>(pf - from_bits<ACT>(pb));
+        uint16_t term[kWeightTerms];
+        split_weight<ACT>(pf, term);
+#pragma unroll
+        for (int i = 0; i < kWeightTerms; ++i)
+          *reinterpret_cast<uint16_t*>(pbuf + p_offset(i * kMaxG + p, row)) = term[i];
         l_part[p] = fmaf(l_part[p], scale, pf);
         m_run[p] = m_new;
         prev_scale[p] = scale;

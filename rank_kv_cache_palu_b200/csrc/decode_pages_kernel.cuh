@@ -13,7 +13,7 @@
 //     once and the pipeline runs on from list to list.  A segment's last value sums are
 //     folded in the next segment's first tile, where its partial is written.
 //   - The rotated query changes with the segment: three buffers, filled two tiles ahead.
-//   - The softmax weights reach the value MMA as hi + lo 16-bit numbers.
+//   - The softmax weights reach the value MMA as sums of three 16-bit numbers (split_weight).
 //   - The MMA warp runs its loop converged and one lane issues.  With the loop on one lane
 //     its operands went through lane registers and every group of MMAs took 700 to 850 cycles
 //     to issue, which set the tile period (16 queries x 32 pages bf16: 170 us; with descriptors
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       float* red = reinterpret_cast<float*>(sbase + L.red);
       constexpr float kLn2 = 0.6931471805599453f;
 
-      // The value sums of tile j sit in the TMEM slot of tile j + 1 (columns [32·mb, +16); column
-      // hw of each block for this head's hi parts of P, hw + 2 for the lo parts); fold them into
+      // The value sums of tile j sit in the TMEM slot of tile j + 1 (columns [32·mb, +16); columns
+      // hw, hw + 2 and hw + 4 of each block for the terms of this head's weights); fold them into
       // the running sums.
       auto fold_at = [&](int j) -> bool {
         if (!mbar_wait(bar(BAR_AT_FULL), j & 1, abort_flag, st, 30)) return false;
@@ -437,8 +437,9 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         for (int mb = 0; mb < NRV; ++mb) {
           const float v = tmem_ld1(tmem + lane_addr + sb + mb * 32 + hw);
           const float w = tmem_ld1(tmem + lane_addr + sb + mb * 32 + hw + 2);
+          const float x = tmem_ld1(tmem + lane_addr + sb + mb * 32 + hw + 4);
           tmem_wait_ld();
-          acc[mb] = fmaf(acc[mb], prev_scale, v + w);
+          acc[mb] = fmaf(acc[mb], prev_scale, v + (w + x));
         }
         return true;
       };
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
           if (row == 0) out[0] = m * kLn2;
           if (lane == 0) out[1 + q4] = l;
 #pragma unroll
-          for (int mb = 0; mb < NRV; ++mb) out[kPartHead + mb * 128 + vrow] = acc[mb];
+          for (int mb = 0; mb < NRV; ++mb) out[kPartHead + mb * 128 + vrow] = acc[mb] * (1.f / kWeightScale<ACT>);
         }
 #pragma unroll
         for (int mb = 0; mb < NRV; ++mb) acc[mb] = 0.f;
@@ -512,13 +513,14 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
         const float m_new = fmaxf(m_run, mt);
         // 0 on a segment's first tile; 1 while every token so far is masked
         const float scale = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);
-        // the weight as hi + lo 16-bit numbers, rows hw and hw + 2 of the value MMA's 16 (its
-        // padding rows are paid for anyway): no weight is rounded to 16 bits
+        // the weight's three terms, rows hw, hw + 2 and hw + 4 of the value MMA's 16
         const float pf = valid ? exp2f(sc - m_new) : 0.f;
-        const uint16_t pb = to_bits<ACT>(pf);
+        uint16_t term[kWeightTerms];
+        split_weight<ACT>(pf, term);
         uint8_t* pbuf = sbase + L.p + slot * kPBytes;
-        *reinterpret_cast<uint16_t*>(pbuf + p_offset(hw, row)) = pb;
-        *reinterpret_cast<uint16_t*>(pbuf + p_offset(hw + 2, row)) = to_bits<ACT>(pf - from_bits<ACT>(pb));
+#pragma unroll
+        for (int i = 0; i < kWeightTerms; ++i)
+          *reinterpret_cast<uint16_t*>(pbuf + p_offset(hw + 2 * i, row)) = term[i];
         l_part = fmaf(l_part, scale, pf);
         m_run = m_new;
         fence_proxy_async();

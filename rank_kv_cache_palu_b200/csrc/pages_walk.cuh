@@ -133,6 +133,23 @@ inline cudaLaunchAttribute dependent_launch() {
   return at;
 }
 
+// A softmax weight reaches the 16-bit value MMA as the sum of three numbers of its type, rows of the
+// product that padding would take anyway: 24 significant bits in bf16, as in float32, 33 in f16.  F16
+// weights are scaled by 2^15 (the largest, 1, still fits), or those below 2^-25 would vanish beside a
+// large one, however many they are.
+constexpr int kWeightTerms = 3;
+template <int ACT> constexpr float kWeightScale = ACT == PALU_F16 ? 0x1p15f : 1.f;
+template <int ACT>
+__device__ __forceinline__ void split_weight(float p, uint16_t (&term)[kWeightTerms]) {
+  float rest = p * kWeightScale<ACT>;
+#pragma unroll
+  for (int i = 0; i < kWeightTerms; ++i) {
+    const auto v = Dt<ACT>::from_f(rest);
+    term[i] = *reinterpret_cast<const uint16_t*>(&v);
+    rest -= Dt<ACT>::to_f(v);       // exact
+  }
+}
+
 // Partial of the segment that tile t ends, for head hl of the launch:
 // m, l of the four warps, then a[r_v] (float32).
 __device__ __forceinline__ float* segment_part(const DecodeArgs& a, const Tile& t, int hl) {

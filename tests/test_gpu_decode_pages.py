@@ -7,6 +7,7 @@ two 16-bit numbers by 2^-16: together 1.2e-4 Σ p|v|.  In float32 angles are cor
 bound is 2e-5 Σ p|v|.  Log-sum-exps are off by at most the score error, 1e-4 (1e-5 in float32).
 """
 import dataclasses
+import math
 
 import numpy as np
 import pytest
@@ -338,3 +339,68 @@ def test_norope_ranks_per_group_up_to_the_largest(ranks_k):
                 off = np.abs(out[i, j, hs] - ref)
                 assert (off <= HALF_STEP[w.act_dtype] * np.abs(ref) + SUM[w.act_dtype] * size).all()
                 np.testing.assert_allclose(lse[i, j, hs], rl, rtol=0, atol=LSE[w.act_dtype])
+
+
+def one_channel(name, T, a, v, **kw):
+    """A case whose scores are exact: latent entry 0 of token t is a[t], it reaches channel 40 of every
+    head alone, where no angle is left (RoPE's frequencies vanish from channel 32 on at this base), and
+    the query is 8 there.  Value channel j of every head is latent entry j, v[t][j]."""
+    w = dataclasses.replace(CASES[name][0], num_heads=CASES[name][0].group_size, **kw)
+    if w.rope_base:
+        w = dataclasses.replace(w, rope_base=3e38)
+    case = make_decode_case(w, [T])
+    q, q_pos = queries(case, 1)
+    q.zero_()
+    q[..., 40] = 8.0
+    case.B_k.zero_()
+    case.B_v.zero_()
+    for h in range(w.group_size):
+        case.B_k[0, 0, h * 128 + 40] = 1.0
+        case.B_v[0, :128, h * 128:(h + 1) * 128] = torch.eye(128)
+    case.zk[0].zero_()
+    case.zv[0].zero_()
+    case.zk[0][0, :, 0] = torch.as_tensor(a)
+    case.zv[0][0, :, :128] = torch.as_tensor(v)
+    return case, q, q_pos
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope"])
+def test_weights_keep_float32(name):
+    """Sums that cancel show the weights' own error.  Two tokens' weights, exp(-3.425) and exp(-1.978), are
+    7.1e-6 above and 6.8e-6 below what two bf16 numbers hold of them, and the values of the 90 tokens of
+    the one and the 30 of the other take each other away, so a weight of 16 bits is off by 6.9e-6 Σ p|v|.
+    In float32 a score of 5 in base 2 has 5 roundings, 1e-6 of a weight, exp2f 2.4e-7, and the value sums
+    of 8 steps of shuffled tokens 2^-23 each of at most the whole: 3e-6 Σ p|v| bounds them together."""
+    rng = np.random.default_rng(1)
+    kind = rng.permutation(np.array([0] * 8 + [1] * 90 + [2] * 30))
+    a = np.array([0.0, -4.84375, -2.796875])[kind]
+    x = np.exp(8 * np.array([-4.84375, -2.796875]) / math.sqrt(128.0))
+    up = 1 + np.arange(128) / 128
+    down = torch.tensor(90 * x[0] * up / (30 * x[1])).to(torch.bfloat16).double().numpy()
+    v = np.where(kind[:, None] == 1, up, np.where(kind[:, None] == 2, -down, 0.0))
+    case, q, q_pos = one_channel(name, 128, a, v)
+    out, _ = run(case, build_pools(case), q, q_pos, [[[[0]]]], 1)
+    ref, _, size = S.decode_attention_pages(q[0, 0].double().numpy(), 127, *case.oracle_latents(0), case.positions(0),
+                                            case.B_k.double().numpy(), case.B_v.double().numpy(), case.w.group_size,
+                                            case.w.rope_base, [[0]], 128, False)
+    assert (np.abs(ref / size).min(1) < 1e-4).all()               # the sums do cancel
+    assert (np.abs(out[0, 0] - ref) <= HALF_STEP["bf16"] * np.abs(ref) + 3e-6 * size).all()
+
+
+@pytest.mark.parametrize("name", ["f16_r256", "norope_f16_r256"])
+def test_many_small_weights_beside_a_large_one(name):
+    """A token that takes nearly all the weight and has no value, beside 999 of weight 2^-25.5 each: below
+    the least f16 number, and all of the result.  A score of 25.5 in base 2 has 5 roundings: 5.3e-6."""
+    T = 1000
+    a = np.full(T, -25.0)
+    a[517] = 0.0
+    v = np.full((T, 128), 1000.0)
+    v[517] = 0.0
+    case, q, q_pos = one_channel(name, T, a, v)
+    lists = [[[list(range(8))]]]
+    out, _ = run(case, build_pools(case), q, q_pos, lists, 8)
+    ref, _, size = S.decode_attention_pages(q[0, 0].double().numpy(), T - 1, *case.oracle_latents(0), case.positions(0),
+                                            case.B_k.double().numpy(), case.B_v.double().numpy(), case.w.group_size,
+                                            case.w.rope_base, lists[0][0], 128, False)
+    assert (0.01 < ref).all()
+    assert (np.abs(out[0, 0] - ref) <= HALF_STEP["f16"] * np.abs(ref) + 1e-5 * size).all()
