@@ -35,7 +35,9 @@ constexpr int kNZK = 6;             // z_k ring stages
 constexpr int kNZV = 4;             // z_v ring stages (pairs of column blocks)
 constexpr int kNQ = 3;              // folded-query buffers
 constexpr int kStageBytes = kTile * kChunk * 2;   // 16 KB: one column block of a page
-constexpr int kN = 16;              // score MMA columns: q̃ hi rows 0-3, lo rows 4-7, 8 padding rows
+constexpr int kN = 16;              // score MMA columns: the terms of q̃, heads in rows 0-3, 4-7, 8-11, padding
+constexpr int kQRows = kFoldTerms * kMaxG;
+static_assert(kQRows <= kN, "a row for each term of each head's query");
 constexpr int kNP = 16;             // value MMA columns: the weights' terms, heads in rows 0-3, 4-7, 8-11, padding
 static_assert(kWeightTerms * kMaxG <= kNP, "a row for each term of each head's weights");
 constexpr int kPBytes = kNP * kTile * 2;
@@ -172,16 +174,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
-      // the folded query of the segment that tile k begins: rows 0-7 of each chunk's 16
+      // the folded query of the segment that tile k begins: the first kQRows of each chunk's 16 rows
       auto push_q = [&](int k) -> bool {
         ++seg;
         const int qb = seg % kNQ;
         if (!mbar_wait(bar(F_QT_EMPTY + qb), ((seg / kNQ) & 1) ^ 1, abort_flag, st, 12)) return false;
-        mbar_expect_tx(bar(F_QT_FULL + qb), (uint32_t)nkc * 1024);
-        const uint8_t* src = static_cast<const uint8_t*>(qt) +
-                             ((size_t)tiles[k].unit * gm.n + gi) * 2 * kMaxG * a.r_k * 2;   // units 16·a.r_k bytes apart
+        mbar_expect_tx(bar(F_QT_FULL + qb), (uint32_t)nkc * kQRows * 128);
+        const uint8_t* src = static_cast<const uint8_t*>(qt) + ((size_t)tiles[k].unit * gm.n + gi) * kQRows * a.r_k * 2;
         for (int c = 0; c < nkc; ++c)
-          bulk_load(base + L.qt + qb * qt_bytes + c * kN * 128, src + (size_t)c * 1024, 1024, bar(F_QT_FULL + qb));
+          bulk_load(base + L.qt + qb * qt_bytes + c * kN * 128, src + (size_t)c * kQRows * 128, kQRows * 128,
+                    bar(F_QT_FULL + qb));
         ++q_issued;
         return true;
       };
@@ -365,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.causal && a.pos_pool != nullptr) pos = t.page >= 0 ? a.pos_pool[(size_t)t.page * a.P + row] : 0;
       if (!mbar_wait(bar(F_D_FULL + slot), (k >> 1) & 1, abort_flag, st, 31)) { ok = false; break; }
       tc_fence_after();
-      float d[2 * kMaxG];
-      tmem_ld8(tmem + lane_addr + slot * kN, d);
+      float d[kN];
+      tmem_ld16(tmem + lane_addr + slot * kN, d);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sc[kMaxG];
 #pragma unroll
       for (int p = 0; p < kMaxG; ++p) {
-        sc[p] = valid && p < gs ? d[p] + d[kMaxG + p] : -INFINITY;   // hi and lo parts of q̃
+        sc[p] = valid && p < gs ? d[p] + (d[kMaxG + p] + d[2 * kMaxG + p]) : -INFINITY;   // the terms of q̃
         float m = sc[p];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -447,6 +449,10 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+size_t pages_query_bytes(const palu_config* c, int units) {
+  return (size_t)units * (c->num_heads / c->group_size) * kQRows * c->rank_k * 2;
+}
 
 cudaError_t launch_decode_pages_fused(const DecodeArgs& a, cudaStream_t st) {
   if (a.act == PALU_BF16) return a.r_v == 256 ? launch_t<PALU_BF16, 2>(a, st) : launch_t<PALU_BF16, 1>(a, st);

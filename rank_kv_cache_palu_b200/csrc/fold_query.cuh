@@ -18,9 +18,11 @@ constexpr int kMaxG = 4;            // heads per group the fused kernels take
 // B_k[g][j][h·d_h, +d_h) in registers and takes its dot product with each
 // query.
 constexpr int kFoldSeqs = 4;
-// IMAGE: the rows are stored as the 128-byte-swizzled K-major operand they become in
-// shared memory, [64-entry chunk][8 rows][128 bytes], so that a bulk copy brings them
-// there (the sparse kernel changes queries as it goes).
+// IMAGE: three terms instead of two (rows h, 4 + h, 8 + h: 24 significant bits in bf16, as in
+// float32; in f16 what is left below 2^-24 is dropped), stored as the 128-byte-swizzled K-major
+// operand they become in shared memory, [64-entry chunk][12 rows][128 bytes], so that a bulk copy
+// brings them there (the sparse kernel changes queries as it goes).
+constexpr int kFoldTerms = 3;
 template <int ACT, bool IMAGE>
 __global__ void __launch_bounds__(256) fold_query_kernel(const __grid_constant__ DecodeArgs a, int qslots, void* qt) {
   using TA = typename Dt<ACT>::T;
@@ -74,16 +76,16 @@ __global__ void __launch_bounds__(256) fold_query_kernel(const __grid_constant__
       acc1 = fmaf(Dt<ACT>::to_f(e[7]), qb.w, acc1);
     }
     float acc = (acc0 + acc1) * sc;
-    const TA hi = Dt<ACT>::from_f(acc);
-    const TA lo = Dt<ACT>::from_f(acc - Dt<ACT>::to_f(hi));
-    TA* out = reinterpret_cast<TA*>(qt) + ((size_t)(v0 + bb) * a.gm.n + gi) * 2 * kMaxG * a.r_k;
-    if constexpr (IMAGE) {
-      TA* chunk = out + (size_t)jb * 8 * 64;
-      chunk[h * 64 + ((jl >> 3) ^ h) * 8 + (jl & 7)] = hi;
-      chunk[(kMaxG + h) * 64 + ((jl >> 3) ^ (kMaxG + h)) * 8 + (jl & 7)] = lo;
-    } else {
-      out[(size_t)h * a.r_k + j] = hi;
-      out[(size_t)(kMaxG + h) * a.r_k + j] = lo;
+    constexpr int kTerms = IMAGE ? kFoldTerms : 2;
+    TA* out = reinterpret_cast<TA*>(qt) + ((size_t)(v0 + bb) * a.gm.n + gi) * kTerms * kMaxG * a.r_k;
+    if constexpr (IMAGE) out += (size_t)jb * kTerms * kMaxG * 64;
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i) {
+      const TA term = Dt<ACT>::from_f(acc);
+      acc -= Dt<ACT>::to_f(term);
+      const int n = i * kMaxG + h;
+      if constexpr (IMAGE) out[n * 64 + ((jl >> 3) ^ (n & 7)) * 8 + (jl & 7)] = term;
+      else out[(size_t)n * a.r_k + j] = term;
     }
   }
 }

@@ -359,7 +359,7 @@ WalkPlan walk_plan(const palu_config* c, int kind, int batch, int Q, int list_le
   p.part = align256((size_t)p.units * heads * stride);
   p.cont = align256((size_t)p.ctas * heads * stride);
   p.segments = align256((size_t)p.units * groups * sizeof(int2));
-  p.folded = kind == 3 ? align256(palu::fused_query_bytes(c, p.units)) : 0;
+  p.folded = kind == 3 ? align256(palu::pages_query_bytes(c, p.units)) : 0;
   return p;
 }
 

@@ -19,6 +19,7 @@ cudaError_t launch_decode_tc_int4(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_decode_pages_tc(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_decode_pages_tc_int4(const DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_decode_pages_fused(const DecodeArgs& a, cudaStream_t st);
+size_t pages_query_bytes(const palu_config* c, int units);   // folded queries of a walk without RoPE
 
 // Decode without RoPE: the key up-projection folded into the query, scores
 // taken on the cached latents (no key is rebuilt).  Its workspace adds the

@@ -404,3 +404,24 @@ def test_many_small_weights_beside_a_large_one(name):
                                             case.w.rope_base, lists[0][0], 128, False)
     assert (0.01 < ref).all()
     assert (np.abs(out[0, 0] - ref) <= HALF_STEP["f16"] * np.abs(ref) + 1e-5 * size).all()
+
+
+@pytest.mark.parametrize("name", ["norope", "norope_f16_r256"])
+def test_folded_queries_keep_float32(name):
+    """One token a sequence: its log-sum-exp is its score, one product q B_k z of up to 40 on entry 0.
+    Scale, query and product are rounded 6 times in float32, 2^-24 of the score each, and to natural
+    logarithms twice more; an f16 query keeps 2^-25 of its own, z = 40 times that."""
+    w = dataclasses.replace(CASES[name][0], num_heads=4)
+    case = make_decode_case(w, [1] * 16)
+    q, q_pos = queries(case, 1)
+    q.mul_((torch.arange(128) == 40).to(q.dtype)).mul_(4.0)
+    case.B_k.zero_()
+    for h in range(4):
+        case.B_k[0, 0, h * 128 + 40] = 1.0
+    for z in case.zk:
+        z.zero_()
+        z[0, 0, 0] = 40.0
+    _, lse = run(case, build_pools(case), q, q_pos, [[[[0]]]] * 16, 1)
+    ref = q[:, :, :, 40].double().numpy() * 40.0 / math.sqrt(128.0)
+    assert np.abs(ref).max() > 20
+    assert (np.abs(lse - ref) <= 8 * 2.0 ** -24 * np.abs(ref) + (40 * 2.0 ** -25 if w.act_dtype == "f16" else 0)).all()
