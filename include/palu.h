@@ -447,7 +447,9 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
  * be finite on the tensor-core kernels.
  * A list that is not ascending or names a page past the sequence is reported as
  * PALU_ERR_DEVICE_BOUNDS (the result is void).  The softmax weights reach the
- * value product as the sum of three 16-bit numbers, as exact as in float32.
+ * value product as the sum of three 16-bit numbers, as exact as in float32.  Keys
+ * are rotated with sines and cosines that are off by at most 2^-21 (2^-23 on the
+ * CUDA-core kernel).
  * num_splits (0 = automatic) splits the lists of the CUDA-core kernel; the
  * tensor-core kernels deal all listed pages of a head group out in equal shares and
  * take any value.  ranks_k / ranks_v as in the ranked calls.

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
     auto store_query = [&](int seg) {
       const float x1 = Dt<ACT>::to_f(qx1), x2 = Dt<ACT>::to_f(qx2);
       float c = 1.f, s = 0.f;
-      if (a.rope) rope_cs_fast(qx_pos, q_om, c, s);
+      if (a.rope) rope_cs_taylor(qx_pos, q_om, c, s);
       const float sc = a.sm_scale * kLog2e;
       float* o = qr + (seg % 3) * 256 + qh * 128 + qi;
       o[0] = (x1 * c - x2 * s) * sc;
@@ -295,6 +295,11 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
     // on packed fp32 pairs (two frequencies at a time).
     constexpr bool contig = CONTIG;
     float* abuf = reinterpret_cast<float*>(sbase + L.tb) + wg * 384;   // [tile parity][head][A|B|-A][32]
+    // Query and tile start take their angles from Taylor sums, 2^-23.5.  The row's, and a token's at
+    // explicit positions, are the hardware's approximations, off by at most 2^-21: Taylor sums took one
+    // query x 16 pages from 18.1 to 18.7 us (they delay the first tile), and 16 queries x 32 pages at
+    // explicit positions from 165 to 201 us; the outputs came no nearer to float32's (5e-5 of them in
+    // bf16, 2.2e-5 in f16, both by their last rounding).
     f2 crow[16], srow[16];
     if (contig) {
 #pragma unroll
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(threads_of(LAT == PALU_INT4), 1)
       if (row >= 64) return;
       const int f = row & 31, hh = row >> 5;
       float c, sn;
-      rope_cs_fast(t0, t_om, c, sn);
+      rope_cs_taylor(t0, t_om, c, sn);
       const float* q = qr + (seg % 3) * 256 + hh * 128 + wg * 32 + f;
       const float qa = q[0], qb = q[64];
       const float A = c * qa + sn * qb, B = c * qb - sn * qa;

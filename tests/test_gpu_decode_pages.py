@@ -425,3 +425,37 @@ def test_folded_queries_keep_float32(name):
     ref = q[:, :, :, 40].double().numpy() * 40.0 / math.sqrt(128.0)
     assert np.abs(ref).max() > 20
     assert (np.abs(lse - ref) <= 8 * 2.0 ** -24 * np.abs(ref) + (40 * 2.0 ** -25 if w.act_dtype == "f16" else 0)).all()
+
+
+@pytest.mark.parametrize("explicit", [False, True])
+@pytest.mark.parametrize("name", ["bf16", "f16_r256"])
+def test_angles_keep_float32(name, explicit):
+    """A sequence's last token, its key one channel of a pair, scores 90 or more for a query one position on
+    with entries of one size in both channels, so that an angle off by e changes the score by up to e of it.
+    The others score 0: the log-sum-exp is that score, S (cos D + sin D) for an angle D between the two.
+    What changes with the position are the angles of query and tile, good to about 2^-24, that of the row
+    by the hardware's sine (2^-21.4 at most: a third of it as rms is 1.2e-7) and a dozen roundings of
+    2^-24 / sqrt 3 (rms) of at most the score, 1.2e-7: 1.8e-7 of it bounds their spread (the constants'
+    roundings shift all)."""
+    w = CASES[name][0]
+    rng = np.random.default_rng(3)
+    lens = rng.integers(1, 3000, 64).tolist()
+    case = make_decode_case(w, lens, explicit_positions=explicit)
+    q, q_pos = queries(case, 1)
+    q.zero_()
+    case.B_k.zero_()
+    ref = np.empty(w.num_heads)
+    for h in range(w.num_heads):
+        f = (7 * h + 3) % 64
+        q[:, :, h, f], q[:, :, h, f + 64] = 32.0, -32.0
+        case.B_k[h // 4, 0, h % 4 * 128 + f] = 1.0
+        turn = w.rope_base ** (-f / 64)
+        ref[h] = 1024.0 / math.sqrt(128.0) * (math.cos(turn) + math.sin(turn))
+    for z, t in zip(case.zk, lens):
+        z.zero_()
+        z[:, t - 1, 0] = 32.0
+    q_pos = np.array([[case.positions(i)[-1] + 1] for i in range(len(lens))], np.int32)
+    lists = [[[[(t - 1) // 128]] * w.groups] for t in lens]
+    _, lse = run(case, build_pools(case), q, q_pos, lists, 1)
+    off = lse[:, 0] / ref - 1
+    assert np.abs(off.mean()) < 8 * 2.0 ** -24 and off.std() < 1.8e-7, f"{off.mean():.2e} {off.std():.2e}"
