@@ -13,7 +13,10 @@
 // (lanes 0-63 the first head, 64-127 the second) and the same lane of both holds
 // the pair.  Tokens of a page have consecutive positions: the key is rotated by the
 // token's offset within 16 (16 angles a thread keeps in registers), then by the
-// angle of the 16-token run's start.
+// angle of the 16-token run's start.  At explicit positions every token has its own angle,
+// from Taylor sums: the hardware's sine is off by up to 2^-21, and a key outside its box
+// could drop a page that matters (64 pages 33.6 us, 27.3 with the hardware's, in packed
+// pairs 32.4).
 //
 // One CTA keeps the B_k of a head pair (128 KB) and walks pages: a bulk-copy
 // producer streams the page's column blocks through a ring (int4: four warps
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(LAT == PALU_INT4 ? 512 : 384, 1)
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
             float c, s;
-            rope_cs_fast(pp[v], om, c, s);
+            rope_cs_taylor(pp[v], om, c, s);
             const float x = k1[v], y = k2[v];
             k1[v] = x * c - y * s;
             k2[v] = y * c + x * s;

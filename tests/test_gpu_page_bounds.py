@@ -182,3 +182,31 @@ def test_timeout_reports_and_recovers():
     st, detail = P.palu_get_device_status(ws)
     assert st == 6 and detail < 90000
     check(case, run(case.cfg, case, pools, case.B_k), uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16_r64", "tiny_f32"])
+def test_bounds_enclose_entries_that_cancel_at_explicit_positions(name):
+    """One token a page, its key 1 in both channels of a pair, at positions where the rotated entry cos - sin
+    nearly vanishes: its outward rounding hides nothing then.  Sine and cosine are good to 2^-23.5 each, the
+    products and the difference of two near numbers are exact."""
+    w = CASES[name]
+    half = w.head_dim // 2
+    pick = []
+    for f in (1, 5, 9, 13):
+        p = np.arange(1, 2 ** 22, dtype=np.int64)
+        x = np.abs(np.remainder(p * w.rope_base ** (-f / half), 2 * np.pi) - np.pi / 4)
+        pick += [(f, int(i)) for i in p[np.argsort(x)[:60]]]
+    case = make_decode_case(w, [1] * len(pick), explicit_positions=True)
+    case.pos = [np.array([p], np.int32) for _, p in pick]
+    case.B_k.zero_()
+    for i, f in enumerate((1, 5, 9, 13)):
+        case.B_k[:, i, f] = case.B_k[:, i, f + half] = 1.0
+    for z, (f, _) in zip(case.zk, pick):
+        z.zero_()
+        z[:, 0, (f - 1) // 4] = 1.0
+    got = run(case.cfg, case, build_pools(case), case.B_k).double().cpu().numpy()
+    for i, (f, p) in enumerate(pick):
+        k = S.page_keys(np.ones((1, 1)), [p], np.eye(w.head_dim)[[f]] + np.eye(w.head_dim)[[f + half]], w.head_dim, w.rope_base)[0]
+        assert abs(k[f]) < 1e-4
+        lo, hi = got[case.page_table[i, 0], 0][:, [f, f + half]]
+        assert (lo <= k[[f, f + half]] + 2 * 2.0 ** -23.5).all() and (hi >= k[[f, f + half]] - 2 * 2.0 ** -23.5).all(), f"{f} {p}"
