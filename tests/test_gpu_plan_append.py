@@ -1,5 +1,8 @@
 """palu_plan_append on the GPU against the CPU oracle: every output is a whole number and equal."""
+import os
 import random
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -210,3 +213,19 @@ def test_quotients_by_any_page_size(page, wide):
         p = Plan(page, [length], table, stack, wide - had, n)
         p.call(torch.tensor([n], dtype=torch.int32, device="cuda"))
         p.check(S.plan_append(page, [n], [length], table, stack, wide - had, n))
+
+
+@pytest.mark.parametrize("rows", [0, 90000])
+def test_batches_around_the_default_shared_memory(rows):
+    """In a process of its own: no larger call has raised the kernel's limit before."""
+    code = f"""
+import random, sys
+sys.path[:0] = {[os.path.dirname(os.path.abspath(__file__)), os.path.dirname(os.path.dirname(os.path.abspath(__file__)))]!r}
+import test_gpu_plan_append as T
+for batch in (3054, 3055, 3071, 3075, 3054):
+    new = [1] * batch
+    new[7] += {rows}
+    T.run_case(random.Random(batch), batch, 8, 4 if not {rows} else 12000, 20000 if {rows} else batch * 4, new, None, fill=0.3 if not {rows} else 1e-4)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
