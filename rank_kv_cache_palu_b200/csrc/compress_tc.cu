@@ -557,6 +557,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   });
+  bind_context();
   return fn;
 }
 

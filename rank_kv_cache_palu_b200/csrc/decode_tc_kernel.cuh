@@ -1082,6 +1082,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
+  bind_context();
   return fn;
 }
 

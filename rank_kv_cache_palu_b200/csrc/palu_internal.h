@@ -144,6 +144,13 @@ cudaError_t launch_select(const palu_config* c, int batch, int num_queries, cons
 // PALU_OK, or PALU_ERR_CUDA with the error's text kept for palu_last_cuda_error.
 palu_status cuda_status(cudaError_t e);
 
+// Makes the current device's context current to the calling host thread.  The driver's tensor-map encoder
+// fails without one, and a thread whose first CUDA call is one of this library's has none yet.
+inline void bind_context() {
+  int device = 0;
+  if (cudaGetDevice(&device) == cudaSuccess) cudaSetDevice(device);
+}
+
 // Counts kernel launches (palu_kernel_launches); call once per launch.
 void count_launch(int n = 1);
 
