@@ -594,7 +594,7 @@ cudaError_t launch_t(const CompressArgs& a, cudaStream_t st) {
   if (p.ntt >= 2 && p.KS == 1) {
     // prefill: persistent, one CTA per SM over every tile
     auto kern = compress_tc_persistent_kernel<ACT, LAT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(kern, smem);
     if (e != cudaSuccess) return e;
     const int tiles = (p.tk + p.tv) * p.ntt;
     kern<<<tiles < 148 ? tiles : 148, kThreads, smem, st>>>(tm_ak, tm_av, tm_x, t);
@@ -602,7 +602,7 @@ cudaError_t launch_t(const CompressArgs& a, cudaStream_t st) {
     return cudaGetLastError();
   }
   auto kern = compress_tc_kernel<ACT, LAT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.tk + p.tv, p.ntt, p.KS);
   kern<<<grid, kThreads, smem, st>>>(tm_ak, tm_av, tm_x, t);

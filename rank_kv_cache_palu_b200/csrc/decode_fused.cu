@@ -501,7 +501,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   const Smem L = smem_layout<QN>(a.r_k);
   const size_t smem = L.total + 1024;
   auto kern = decode_fused_kernel<ACT, NRV, QN>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   kern<<<dim3(a.S, a.gm.n, a.batch), kThreads, smem, st>>>(a, qt);
   count_launch();

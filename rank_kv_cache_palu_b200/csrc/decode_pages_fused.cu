@@ -434,7 +434,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const size_t smem = fused_smem(a.r_k).total;
   auto kern = decode_pages_fused_kernel<ACT, NRV>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at = dependent_launch();
   cudaLaunchConfig_t c{};

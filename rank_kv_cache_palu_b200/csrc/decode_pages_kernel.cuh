@@ -851,7 +851,7 @@ cudaError_t launch_pages_t(const DecodeArgs& a, cudaStream_t st) {
   const size_t smem = pages_smem(a.r_k, LAT == PALU_INT4).total;
   auto kern =
       a.pos_pool == nullptr ? decode_pages_kernel<ACT, NRV, LAT, true> : decode_pages_kernel<ACT, NRV, LAT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   if constexpr (LAT == PALU_INT4) {
     // the setmaxnreg split needs a launch at kRegsLaunch registers a thread (see decode_tc_kernel.cuh)

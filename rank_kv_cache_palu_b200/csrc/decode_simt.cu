@@ -310,10 +310,8 @@ template <int ACT, int LAT>
 cudaError_t launch_split_t(const DecodeArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(float) * (a.d_h + kTT * (a.r_k + a.r_v + a.d_h) + kTT) + sizeof(int) * kTT;
   auto kern = split_kernel<ACT, LAT>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_shared(kern, smem);
+  if (e != cudaSuccess) return e;
   dim3 grid(a.S, a.gm.n * a.gs, a.batch);
   kern<<<grid, kThreads, smem, st>>>(a);
   count_launch();

@@ -1144,7 +1144,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t st) {
     args.trace = static_cast<long long*>(ts.buffer);
     args.trace_tiles = ts.tiles;
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   if constexpr (LAT == PALU_INT4) {
     // The warpgroups' setmaxnreg split adds up to exactly the registers of a launch at

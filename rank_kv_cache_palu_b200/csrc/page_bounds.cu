@@ -552,7 +552,7 @@ cudaError_t launch_tc(const BoundsArgs& all, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const size_t smem = layout(all.max_rk).total + 1024;
   auto kern = all.pos_pool == nullptr ? bounds_tc_kernel<ACT, LAT, true> : bounds_tc_kernel<ACT, LAT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(kern, smem);
   if (e != cudaSuccess) return e;
   // one CTA per SM, the same number for every (group, head pair), each with its B_k resident
   const int combos = all.gm.n * (all.gs / 2);

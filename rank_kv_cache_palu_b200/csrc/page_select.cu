@@ -45,6 +45,7 @@ constexpr int kVisit = 2;        // pages a warp sums side by side
 static_assert(kHeads == 2 && kVisit == 2, "the sums of a visit are folded by two");
 constexpr int kSlots = 4;        // pages a warp has in shared memory or on their way there
 constexpr int kRing = 72 * 1024; // shared memory of the warps' slots, at most
+constexpr int kStatic = 4 * 1024;// room for the kernel's static shared memory
 constexpr float kErr = 0x1p-20f; // E over Σ (|q_c| + |q_pair(c)|) |v_c|
 
 struct SelectArgs {
@@ -688,10 +689,8 @@ cudaError_t launch(SelectArgs a, cudaStream_t st) {
   const size_t cut = sizeof(unsigned) * a.max_pages;
   const size_t smem = sizeof(float) * 2 * a.W + (vec && slots > cut ? slots : cut);
   auto kern = vec ? select_kernel<DT, true> : select_kernel<DT, false>;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_shared(kern, smem, kStatic);
+  if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, st>>>(a);
   count_launch();
   return cudaGetLastError();

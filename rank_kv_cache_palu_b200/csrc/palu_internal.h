@@ -144,6 +144,15 @@ cudaError_t launch_select(const palu_config* c, int batch, int num_queries, cons
 // PALU_OK, or PALU_ERR_CUDA with the error's text kept for palu_last_cuda_error.
 palu_status cuda_status(cudaError_t e);
 
+// Lets a launch of `kernel` take `bytes` of dynamic shared memory, beside at most `fixed` bytes of the kernel's
+// own.  The limit is state of the kernel on the device, so every call sets the same one, the largest there
+// is: with a limit of its own, a call could lower it between another host thread's and that one's launch.
+template <class K>
+cudaError_t allow_shared(K* kernel, size_t bytes, size_t fixed = 0) {
+  if (bytes + fixed <= 48 * 1024) return cudaSuccess;       // what every launch may take
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(227 * 1024 - fixed));
+}
+
 // Makes the current device's context current to the calling host thread.  The driver's tensor-map encoder
 // fails without one, and a thread whose first CUDA call is one of this library's has none yet.
 inline void bind_context() {

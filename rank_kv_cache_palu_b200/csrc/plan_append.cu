@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kStatic = 512;      // room for the kernel's static shared memory
 
 // Quotients by the page size, which is known only at run time: n / P = (n·m) >> s for
 // 0 <= n < 2^31 with s = 31 + ceil(log2 P) and m = ceil(2^s / P) (m·P exceeds 2^s by less
@@ -283,11 +284,8 @@ constexpr int kSmall = 148 * kThreads;
 template <int ROWS>
 cudaError_t launch(const PlanArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(int32_t) * (4 * (size_t)a.batch + 1);
-  if (smem > 40 * 1024) {      // with the kernel's static shared memory past the 48 KB every launch may take
-    const cudaError_t e =
-        cudaFuncSetAttribute(plan_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_shared(plan_kernel<ROWS>, smem, kStatic);
+  if (e != cudaSuccess) return e;
   const long long per = (long long)kThreads * ROWS;
   long long grid = (a.n_rows + per - 1) / per;
   grid = grid < 1 ? 1 : grid > 8 * 148 ? 8 * 148 : grid;

@@ -102,3 +102,44 @@ def test_a_thread_of_no_cuda_call_before(make):
     t.join()
     torch.cuda.synchronize()
     assert not failed, failed[0]
+
+
+def raw(make, large, stream, monkeypatch):
+    """The library call that make's call comes to, with its arguments: nothing of Python's between two."""
+    call, lib, seen = make(large), P.load(), []
+
+    class Recorder:
+        def __getattr__(self, name):
+            fn = getattr(lib, name)
+            return lambda *a: seen.append((fn, a)) or fn(*a)
+
+    with monkeypatch.context() as m:
+        m.setattr(P, "load", Recorder)
+        call(stream)
+    return seen[-1] + (call,)
+
+
+@pytest.mark.parametrize("make", EVERY, ids=lambda f: f.__name__)
+def test_sizes_of_two_threads(make, monkeypatch):
+    """None of two calls may lower what the other's launch is allowed."""
+    calls, failed = [], []
+    for large in (False, True):
+        stream = torch.cuda.Stream()
+        calls.append((stream, *raw(make, large, stream, monkeypatch)))
+    torch.cuda.synchronize()
+
+    def work(stream, fn, args, _):
+        for n in range(5000):
+            if fn(*args) != 0:
+                failed.append(P.load().palu_last_cuda_error().decode())
+                return
+            if n % 256 == 255:
+                stream.synchronize()
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed[0]
