@@ -15,6 +15,8 @@
 //   |ŝ - s| <= E = 2^-20 Σ_c (|q_c| + |q_pair(c)|) |v_c|  (|v_c|: the largest of the list's pages):
 // 9 roundings of a sum of up to 9 steps, 9·2^-24 Σ|q'_c v_c|, and 2^-21.5 (|q_c| +
 // |q_pair(c)|) for the rotated query (angle 2^-23, sine and cosine 2^-23, two products).
+// Where |q'_c| is no more than that error its sign, and so the side of the box, may be
+// another in float64: |v_c| is the larger of the two sides there.
 // With T̂ the float32 threshold the float64 one lies within E of it, so a page more
 // than 2 E above T̂ is in, one more than 2 E below it is out, and only where pages
 // inside that band have to be told apart are their float64 scores taken (about one
@@ -82,6 +84,9 @@ __device__ __forceinline__ int pages_seen(const SelectArgs& a, int T, int qpos) 
   if (a.causal && (long long)qpos + 1 < t) t = max(0LL, (long long)qpos + 1);
   return (int)((t + a.P - 1) / a.P);
 }
+
+// Whether a float32 rotated query entry q of |q_c| + |q_pair(c)| = n may have the other sign in float64.
+__device__ __forceinline__ bool unsure(float q, float n) { return n > 0.f && !(fabsf(q) > 0x1p-21f * n); }
 
 // Order-preserving keys of scores (no NaN), never 0, and back.
 __device__ __forceinline__ unsigned long long key_of(double v) {
@@ -246,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
   }
 
   if (p0 < p1) {
+    bool doubt = false;
     for (int i = tid; i < a.gs * half; i += kThreads) {
       const int h = i / half, f = i - h * half;
       if (i >= kThreads) {
@@ -255,11 +261,15 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
       const float u = Dt<DT>::to_f(x1), w = Dt<DT>::to_f(x2);
       float c = 1.f, s = 0.f;
       if (a.rope) rope_cs_accurate(qpos, a.omega[f], c, s);
-      qr[h * a.d_h + f] = u * c - w * s;
-      qr[h * a.d_h + half + f] = w * c + u * s;
-      qn[h * a.d_h + f] = qn[h * a.d_h + half + f] = fabsf(u) + fabsf(w);
+      const float x = u * c - w * s, y = w * c + u * s;
+      float n = fabsf(u) + fabsf(w);
+      if (n > 0.f) n = fmaxf(n, 0x1p-100f);     // roundings of anything less are not relative ones
+      qr[h * a.d_h + f] = x;
+      qr[h * a.d_h + half + f] = y;
+      qn[h * a.d_h + f] = qn[h * a.d_h + half + f] = n;
+      doubt = doubt || unsure(x, n) || unsure(y, n);
     }
-    __syncthreads();
+    doubt = __syncthreads_or(doubt) && a.rope;
     float* mine = out + p0 + warp;
     float err = 0.f;   // what E is taken from, over this warp's pages
     if constexpr (VEC) {
@@ -357,6 +367,24 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
         }
         if (lane == 0) mine[k * kWarps] = best;
       }
+    }
+    if (doubt) {
+      // channels where float64 may take the other side of the box: both sides count, over the warp's pages
+      float most = 0.f;
+      for (int k = 0; k < nk; ++k) {
+        const int pg = __shfl_sync(0xffffffffu, my_page, k);
+        const T* lo = bounds + ((size_t)max(pg, 0) * a.G + g) * 2 * a.W;
+        float e = 0.f;
+        for (int c = lane; c < width && pg >= 0; c += 32) {
+          if (!unsure(qr[c], qn[c])) continue;
+          const float x = fabsf(Dt<DT>::to_f(lo[c])), y = fabsf(Dt<DT>::to_f(lo[a.W + c]));
+          e = fmaf(qn[c], x == x && y == y ? fmaxf(x, y) : INFINITY, e);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+        most = e < INFINITY ? fmaxf(most, e) : INFINITY;
+      }
+      err += most;
     }
     if (lane == 0) werr[warp] = err;
     __syncthreads();

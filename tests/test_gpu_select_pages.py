@@ -6,6 +6,7 @@ most 2^-21.5 (|q_c| + |q_pair(c)|): an angle good to 2π·2^-26 = 2^-23.3, sine 
 two products and a sum to 2·2^-24.  With |q'_c| <= |q_c| + |q_pair(c)| the error is below
 (9·2^-24 + 2^-21.5) Σ (|q_c| + |q_pair(c)|) |v_c| = 0.93·2^-20 of that sum."""
 import dataclasses
+import math
 
 import numpy as np
 import pytest
@@ -211,3 +212,32 @@ def test_an_error_bound_that_overflows(name):
     second[..., 1] = 0.0
     second[..., 8] = 1.0
     check(c, 1, 0, 0, scores=False)
+
+
+@pytest.mark.parametrize("name", ["tiny_f32", "d20_f32"])
+@pytest.mark.parametrize("far", [1e6, float("inf"), float("nan")])
+def test_query_entries_that_cancel_under_rotation(name, far):
+    """u cos - w sin of u = sin, w = cos in float32: the rotated entry is 0 but for roundings, and in float32
+    its sign need not be float64's.  One page's box has nothing on one side of that channel and far on the
+    other: the sign alone tells whether the page wins."""
+    w = dataclasses.replace(SHAPES[name], group_size=1)
+    d, b = w.head_dim, 40
+    half = d // 2
+    c = make(w, [6 * PAGE] * b, seed=2)
+    rng = np.random.default_rng(4)
+    c["q_pos"] = torch.from_numpy(rng.integers(1, 60000, (b, 1)).astype(np.int32))
+    c["q"].zero_()
+    c["bounds"].zero_()
+    for i in range(b):
+        for h in range(w.num_heads):
+            f = int(rng.integers(0, half - 1))
+            turn = int(c["q_pos"][i, 0]) * w.rope_base ** (-f / half)
+            c["q"][i, 0, h, f], c["q"][i, 0, h, f + half] = math.sin(turn), math.cos(turn)
+            for lp in range(6):
+                box = c["bounds"][int(c["table"][i, lp]), h]
+                box[:, f + half] = 1e-3 * (lp + 1)          # the last pages lead by the pair's other channel
+            lp = int(rng.integers(0, 3)) + (3 if math.isnan(far) else 0)     # (NaN drops a page that leads)
+            box = c["bounds"][int(c["table"][i, lp]), h]
+            side = int(rng.integers(0, 2))
+            box[side, f] = far if side else -far
+    check(c, 2, 0, 0, scores=False)
