@@ -335,7 +335,7 @@ palu_status palu_decode_attn_noalloc(const palu_config* cfg, int batch, const vo
  * Refused and reported as PALU_ERR_DEVICE_BOUNDS: a length that would leave
  * [0, max_pages·page_size], or rows past n_rows.  Also reported: a num_free
  * outside [0, num_pages] (taken as 0) and page numbers outside the pool (their
- * rows get slot -1).
+ * rows get slot -1; given back, they do not go onto the stack).
  * batch <= PALU_PLAN_MAX_BATCH (PALU_ERR_UNSUPPORTED above); page_size a multiple
  * of 8; num_pages·page_size below 2^31.  One launch, no synchronisation. */
 #define PALU_PLAN_MAX_BATCH 8192

@@ -41,7 +41,10 @@ def plan_append(page_size, num_new, seq_lens, page_table, free_pages, num_free, 
                 table[b][lp] = stack[num_free - 1 - popped]
                 popped += 1
         for lp in range(has, had):
-            given.append(table[b][lp])
+            if 0 <= table[b][lp] < len(stack):
+                given.append(table[b][lp])
+            else:
+                fault = True
             table[b][lp] = -1
         for j in range(max(n, 0)):
             t = old + j

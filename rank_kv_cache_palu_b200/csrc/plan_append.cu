@@ -260,16 +260,34 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
       if (b < a.batch) start[b] = (int)min(j0, (long long)INT32_MAX);
     }
     __syncthreads();
+    bool bad = false;
     for (long long j = tid; j < given; j += kThreads) {
       const int lo = last_from(start, a.batch, j);   // the sequence of page j
       const int lp = pages_of(a, len[lo] + take[lo]) + (int)(j - start[lo]);
       int32_t* entry = a.page_table + (size_t)lo * a.max_pages + lp;
       const int page = *entry;
       *entry = -1;
-      if (page < 0 || page >= a.num_pages) report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + lo);
+      if (page < 0 || page >= a.num_pages) {
+        report(a.st, PALU_ERR_DEVICE_BOUNDS, 6000000 + lo);
+        bad = true;
+      }
       const long long at = left + given - 1 - j;
       if (at < a.num_pages) a.free_pages[at] = page;
       else report(a.st, PALU_ERR_DEVICE_BOUNDS, 4000001);   // more pages given back than the pool has
+    }
+    if (__syncthreads_or(bad)) {
+      // numbers outside the pool among them: the others close up
+      const long long end = min(left + given, (long long)a.num_pages);
+      long long top = left;
+      for (long long i0 = left; i0 < end; i0 += kThreads) {
+        const int page = i0 + tid < end ? a.free_pages[i0 + tid] : -1;
+        const bool good = page >= 0 && page < a.num_pages;
+        long long total;
+        const long long at = top + block_scan(good, warp_sums, total);   // (every thread has read by its first barrier)
+        if (good) a.free_pages[at] = page;
+        top += total;
+      }
+      given = top - left;
     }
   }
   for (int b = tid; b < a.batch; b += kThreads)

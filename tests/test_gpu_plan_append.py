@@ -229,3 +229,25 @@ for batch in (3054, 3055, 3071, 3075, 3054):
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("pages", [3, 700])
+def test_bad_pages_given_back_stay_off_the_stack(pages):
+    rng = random.Random(13)
+    table = [rng.sample(range(3 * pages), pages), [], list(range(3 * pages, 4 * pages))]
+    table[1] = [p for p in range(3 * pages) if p not in set(table[0])][:pages]
+    used = set(sum(table, []))
+    stack = [p for p in range(4 * pages) if p not in used]
+    had = len(stack)
+    stack += [-1] * (4 * pages - had)
+    for b in range(3):
+        for lp in rng.sample(range(pages), 1 + pages // 5):
+            table[b][lp] = rng.choice([-1, -5, 4 * pages, 2 ** 31 - 1])
+    lens, new = [8 * pages] * 3, [-8 * pages, 0, -8 * (pages - 1)]
+    p = Plan(8, lens, table, stack, had, 0)
+    p.call(torch.tensor(new, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    ref = S.plan_append(8, new, lens, table, stack, had, 0)
+    assert ref["fault"] and P.palu_get_device_status(p.ws)[0] == 7
+    assert int(p.free) == ref["num_free"] and p.stack.tolist()[:ref["num_free"]] == ref["free_pages"][:ref["num_free"]]
+    assert p.table.tolist() == ref["page_table"] and p.lens.tolist() == ref["seq_lens"]
