@@ -458,13 +458,13 @@ def _layer(cfg: PaluConfig, ranks_k=None, ranks_v=None) -> _Layer:
     return made
 
 
-def _pool(A, name, pool, num_pages, page_bytes):
-    """A cache pool that holds at least num_pages pages."""
+def _pool(A, name, pool, num_pages, page_bytes, dtype=None):
+    """A cache pool that holds at least num_pages pages (latents and scales: bytes of any type)."""
     if pool is None:
         return None
     if pool.nbytes < num_pages * page_bytes:
         raise ValueError(f"{A.where}: {name} holds fewer than {num_pages} pages")
-    return A(name, pool, None)
+    return A(name, pool, dtype)
 
 
 def _sized(A, name, t, dtype, entries):
@@ -497,7 +497,7 @@ def palu_page_bounds(cfg: PaluConfig, first, zk_pool, zk_scales, pos_pool, page_
     table, lens = A.take(("page_table", "seq_lens"), (page_table, seq_lens), [_I32, _I32], [(batch, max_pages), (batch,)])
     A.call(load().palu_page_bounds, ctypes.byref(cfg), _ranks(ranks_k), batch, A("first", first, _I32, (batch,)),
            _pool(A, "zk_pool", zk_pool, num_pages, L.zk), _pool(A, "zk_scales", zk_scales, num_pages, L.zks),
-           _pool(A, "pos_pool", pos_pool, num_pages, L.pos), table, max_pages, lens, num_pages,
+           _pool(A, "pos_pool", pos_pool, num_pages, L.pos, _I32), table, max_pages, lens, num_pages,
            _sized(A, "B_k", B_k, L.act, L.rows_k), _bounds(A, bounds, L.act, num_pages * L.bounds),
            A("workspace", workspace, None), workspace.nbytes, stream=stream)
 
@@ -554,7 +554,7 @@ def palu_decode_attn_pages(cfg: PaluConfig, q, q_pos, zk_pool, zv_pool, zk_scale
     A.call(load().palu_decode_attn_pages, ctypes.byref(cfg), _ranks(ranks_k), _ranks(ranks_v), batch, Q, query, at,
            _pool(A, "zk_pool", zk_pool, num_pages, L.zk), _pool(A, "zv_pool", zv_pool, num_pages, L.zv),
            _pool(A, "zk_scales", zk_scales, num_pages, L.zks), _pool(A, "zv_scales", zv_scales, num_pages, L.zvs),
-           _pool(A, "pos_pool", pos_pool, num_pages, L.pos), table, max_pages, lens, lists, counts, keep, num_pages,
+           _pool(A, "pos_pool", pos_pool, num_pages, L.pos, _I32), table, max_pages, lens, lists, counts, keep, num_pages,
            _sized(A, "B_k", B_k, L.act, L.rows_k), _sized(A, "B_v", B_v, L.act, L.rows_v), result,
            A("lse", lse, _F32, rows[:3]), A("workspace", workspace, None), workspace.nbytes, num_splits, stream=stream)
 

@@ -258,3 +258,18 @@ def test_binding_checks_the_number_of_ranks():
     empty.group_size = 0
     with pytest.raises(P.PaluError):
         P.palu_decode_pages_workspace_size(empty, 1, 1, 4)
+
+
+def test_binding_takes_int32_positions_only():
+    c = cfg(num_heads=4)
+    bf = torch.bfloat16
+    zk, bounds, Bk = ws(128 * 512), torch.zeros(2 * 512, dtype=bf), torch.zeros((256, 512), dtype=bf)
+    q, pos = torch.zeros((1, 1, 4, 128), dtype=bf), torch.zeros(128, dtype=torch.int64)
+    with pytest.raises(ValueError, match="pos_pool"):
+        P.palu_page_bounds(c, None, zk, None, pos, i32(1, 2), i32(1), 1, Bk, bounds, ws())
+    with pytest.raises(ValueError, match="pos_pool"):
+        P.palu_decode_attn_pages(c, q, i32(1, 1), zk, zk, None, None, pos, i32(1, 2), i32(1), i32(1, 1, 1, 4),
+                                 i32(1, 1, 1), 1, Bk, Bk[:128], q, None, ws())
+    with pytest.raises(ValueError, match="pos_pool"):
+        P.palu_select_pages(c, q, i32(1, 1), bounds, pos, i32(1, 2), i32(1), 1, 0, 0, i32(1, 1, 1, 4), i32(1, 1, 1), None,
+                            ws())
