@@ -407,7 +407,8 @@ palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int
                              palu_stream_t stream);
 
 /* Page selection: for every query and head group the list_len pages of largest
- *   score(page) = max over the group's heads h of Σ_c max(q'_h,c lo_c, q'_h,c hi_c),
+ *   score(page) = max over the group's heads h of Σ_c q'_h,c v_c,
+ *   v_c = hi_c where q'_h,c >= 0, lo_c below (the larger product),
  * q' = R(q_pos) q: an upper bound, times √d_h, of every score the page holds.
  *   q          [batch][num_queries][H][head_dim], q_pos [batch][num_queries]
  *   pos_pool   the cache's position pool or NULL
@@ -421,8 +422,9 @@ palu_status palu_page_bounds(const palu_config* cfg, const int32_t* ranks_k, int
  * A query sees every page of its sequence; with num_queries > 1 and no position
  * pool only those that hold a token at or before q_pos.  The choice is that of
  * scores computed in float64 (page_scores are float32 sums, within 2^-20 Σ_c
- * (|q_c| + |q_pair(c)|) |v_c| of them, v_c the bound taken); of equal scores
- * the lower page wins; a head's sum that is not a number counts as -inf.
+ * (|q_c| + |q_pair(c)|) |v_c| of them, v_c the bound taken, or the larger one where
+ * |q'_c| is below 2^-21 (|q_c| + |q_pair(c)|)); of equal scores the lower page wins; a head's sum that is not a number (0 times an infinite bound
+ * among its products) counts as -inf.  A channel without entries makes its head -inf.
  * batch·num_queries·G <= PALU_SELECT_MAX_LISTS, max_pages <= PALU_SELECT_MAX_PAGES and
  * group_size·head_dim <= 8192 (PALU_ERR_UNSUPPORTED above). */
 #define PALU_SELECT_MAX_LISTS 65536

@@ -1,8 +1,8 @@
 // Page selection: for each query and head group, the pages whose bound on the
 // query's scores is largest.
 //
-//   score(page) = max_h Σ_c max(q'_h,c lo_c, q'_h,c hi_c),   q' = R(q_pos) q,
-// the larger product being q'·hi for q' >= 0 and q'·lo below.
+//   score(page) = max_h Σ_c q'_h,c v_c,   v_c = hi_c where q'_h,c >= 0 and lo_c below,
+// the larger product, q' = R(q_pos) q.
 //
 // One CTA scores a run of pages for one list (sequence, group, query).  A page's 2·W
 // entries of a group are contiguous (2 KB in the 7B shape): every warp streams its
