@@ -459,3 +459,83 @@ def test_angles_keep_float32(name, explicit):
     _, lse = run(case, build_pools(case), q, q_pos, lists, 1)
     off = lse[:, 0] / ref - 1
     assert np.abs(off.mean()) < 8 * 2.0 ** -24 and off.std() < 1.8e-7, f"{off.mean():.2e} {off.std():.2e}"
+
+
+MORE = {
+    "int4_f16_norope": (dataclasses.replace(CASES["int4_f16"][0], rope_base=0.0), 2),
+    "int4_bf16_norope": (dataclasses.replace(CASES["int4_bf16"][0], rope_base=0.0), 2),
+    "norope_d64": (w7b(rope_base=0.0, head_dim=64), 3),
+    "norope_d40_three_heads": (dataclasses.replace(w7b(rope_base=0.0, head_dim=40, group_size=3, rank_k=128), num_heads=6), 3),
+    "norope_one_head": (dataclasses.replace(w7b(rope_base=0.0, group_size=1, rank_v=256), num_heads=2), 3),
+    "eight_heads": (dataclasses.replace(w7b(group_size=8, rank_k=128), num_heads=16), 2),
+    "r192_r256": (w7b(rank_k=192, rank_v=256, act_dtype="f16", latent_dtype="f16"), 2),
+    "f32_r512": (dataclasses.replace(WORKLOADS["tiny_f32"], rank_k=512, rank_v=512, head_dim=128, page_size=40), 1),
+    "f32_r96": (dataclasses.replace(WORKLOADS["tiny_f32"], rank_k=96, rank_v=288), 1),
+}
+
+
+def compare_up(case, out, lse, q, q_pos, lists):
+    """compare() for float32, where a query may see so few tokens that an output channel is nearly nothing:
+    the up-projection then shows its own roundings.  It runs in 8 chains of r_v / 8 terms and 3 joins on
+    sums rounded once: (r_v / 8 + 4)·2^-24 Σ_r |a_r||B_r|, with Σ_r |a_r||B_r| at most the largest token's."""
+    w = case.w
+    for i, j in np.ndindex(*q_pos.shape):
+        zk, zv = case.oracle_latents(i)
+        Bk, Bv = case.B_k.double().numpy(), case.B_v.double().numpy()
+        ref, rl, size = S.decode_attention_pages(q[i, j].double().numpy(), q_pos[i, j], zk, zv, case.positions(i), Bk, Bv,
+                                                 w.group_size, w.rope_base, lists[i][j], w.page_size, q_pos.shape[1] > 1)
+        up = np.zeros((w.num_heads, w.head_dim))
+        for g in range(w.groups):
+            if case.seq_lens[i]:
+                up[g * w.group_size:(g + 1) * w.group_size] = (np.abs(zv[g]) @ np.abs(Bv[g])).max(0).reshape(w.group_size, -1)
+        off = np.abs(out[i, j] - ref)
+        assert (off <= HALF_STEP["f32"] * np.abs(ref) + SUM["f32"] * size + (w.rank_v / 8 + 4) * 2.0 ** -24 * up).all()
+        empty = np.isneginf(rl)
+        assert (np.isneginf(lse[i, j]) == empty).all()
+        np.testing.assert_allclose(lse[i, j][~empty], rl[~empty], rtol=0, atol=LSE["f32"])
+
+
+@pytest.mark.parametrize("Q", [1, 2])
+@pytest.mark.parametrize("name", list(MORE))
+def test_more_shapes(name, Q):
+    w, kind = MORE[name]
+    case = make_decode_case(w, [300, 0, 1, 700])
+    assert P.palu_decode_kernel_kind(case.cfg) == kind
+    q, q_pos = queries(case, Q)
+    lists = pick_lists(case, Q, 4, seed=Q)
+    if w.act_dtype == "f32":
+        compare_up(case, *run(case, build_pools(case), q, q_pos, lists, 4), q, q_pos, lists)
+        return
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 4), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16", "tiny_f32"])
+@pytest.mark.parametrize("keep", [200, 5000])
+def test_few_pages_in_a_long_list(name, keep):
+    case = make_decode_case(CASES[name][0], [300, 0, 900])
+    q, q_pos = queries(case, 2)
+    lists = pick_lists(case, 2, 3)
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, keep), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["bf16", "norope", "int4_f16", "tiny_f32"])
+def test_drafts_that_list_the_same_pages(name):
+    case = make_decode_case(CASES[name][0], [900, 260])
+    q, q_pos = queries(case, 4)
+    lists = pick_lists(case, 1, 4)
+    lists = [[row[0]] * 4 for row in lists]
+    if name == "tiny_f32":
+        compare_up(case, *run(case, build_pools(case), q, q_pos, lists, 4), q, q_pos, lists)
+        return
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 4), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name,Q,keep,batch", [("bf16", 1, 1, 2100), ("norope", 1, 1, 2100), ("norope", 3, 2, 700),
+                                               ("bf16", 2, 1000, 90), ("norope", 2, 1000, 90)])
+def test_more_queries_than_one_launch_walks(name, Q, keep, batch):
+    """Runs of sequences behind one another: past 2048 queries, or past 128 x 148 x 8 list entries."""
+    w = dataclasses.replace(CASES[name][0], num_heads=4, rank_k=64)
+    case = make_decode_case(w, [1 + i * 37 % 260 for i in range(batch)])
+    q, q_pos = queries(case, Q)
+    lists = pick_lists(case, Q, min(keep, 3))
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, keep), q, q_pos, lists, uniform(case))

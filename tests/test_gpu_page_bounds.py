@@ -210,3 +210,22 @@ def test_bounds_enclose_entries_that_cancel_at_explicit_positions(name):
         assert abs(k[f]) < 1e-4
         lo, hi = got[case.page_table[i, 0], 0][:, [f, f + half]]
         assert (lo <= k[[f, f + half]] + 2 * 2.0 ** -23.5).all() and (hi >= k[[f, f + half]] - 2 * 2.0 ** -23.5).all(), f"{f} {p}"
+
+
+@pytest.mark.parametrize("explicit", [False, True])
+@pytest.mark.parametrize("name", ["int4_f16", "int4_bf16", "bf16"])
+def test_bounds_without_rope(name, explicit):
+    case = make_decode_case(dataclasses.replace(CASES[name], rope_base=0.0), [300, 0, 1, 515], explicit_positions=explicit)
+    check(case, run(case.cfg, case, build_pools(case), case.B_k), uniform(case))
+
+
+@pytest.mark.parametrize("ranks_k", [[64, 512], [320, 256]])
+def test_a_key_rank_past_256(ranks_k):
+    """The whole layer takes the CUDA-core kernel."""
+    case = make_ranked_case(w7b(), ranks_k, [128, 128], [140, 9])
+
+    def keys(i):
+        zk, _, Bk, _ = case.oracle_inputs(i)
+        return list(zip(zk, Bk))
+
+    check(case, run(case.cfg, case, build_ranked_pools(case), case.B_k, ranks_k=ranks_k), keys)
