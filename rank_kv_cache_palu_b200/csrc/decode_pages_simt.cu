@@ -38,7 +38,7 @@ __device__ __forceinline__ ListRange list_range(const DecodeArgs& a, int vb, int
     T = T < 0 ? 0 : cap;
   }
   r.T = T;
-  r.npg = (T + a.P - 1) / a.P;
+  r.npg = page_count(T, a.P);
   const size_t li = (size_t)vb * a.G + g;
   const int32_t* list = a.page_list + li * a.list_len;
   int n = a.page_counts[li];

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kKeyThreads) bounds_simt_kernel(const __grid_c
   const int lanes = key_lanes(half), tokens = key_tokens(half);
   const int i = tid % lanes, run = tid / lanes;
   const int T = tokens_of(a, b, tid == 0 && blockIdx.x == 0 && h == 0);
-  const int npg = (T + a.P - 1) / a.P;
+  const int npg = page_count(T, a.P);
   const TA* Bk = reinterpret_cast<const TA*>(a.Bk) + (size_t)a.gm.k_row0[g] * a.W + jh * a.d_h;
   for (int lp = first_page(a, b) + blockIdx.x; lp < npg; lp += gridDim.x) {
     const int page = a.page_table[(size_t)b * a.max_pages + lp];
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(LAT == PALU_INT4 ? 512 : 384, 1)
       int n = 0;
       if (b < a.batch) {
         const int T = tokens_of(a, b, blockIdx.x == 0 && blockIdx.y == 0);
-        n = max(0, (T + a.P - 1) / a.P - first_page(a, b));
+        n = max(0, page_count(T, a.P) - first_page(a, b));
       }
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_kernel(const __grid_consta
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) report(a.st, PALU_ERR_DEVICE_BOUNDS, 1000000 + b);
     T_ = T_ < 0 ? 0 : cap;
   }
-  const int npg = (T_ + a.P - 1) / a.P;
+  const int npg = page_count(T_, a.P);
   const int p1 = min(npg, p0 + a.chunk);
   const T* bounds = static_cast<const T*>(a.bounds);
   const size_t unit = ((size_t)b * a.G + g) * a.Q + j;

@@ -87,7 +87,7 @@ __device__ __forceinline__ int walk_tiles(const DecodeArgs& a, int g, int gi, bo
       report(st, PALU_ERR_DEVICE_BOUNDS, 1000000 + sb);
       T = T < 0 ? 0 : cap;
     }
-    const int npg = (T + a.P - 1) / a.P;
+    const int npg = page_count(T, a.P);
     Tile t;
     t.unit = u;
     t.lp = lp;

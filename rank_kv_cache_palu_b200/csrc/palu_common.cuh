@@ -25,6 +25,9 @@ __device__ __forceinline__ void report(DevStatus* st, int code, int detail) {
   if (st != nullptr && atomicCAS(&st->code, 0, code) == 0) st->detail = detail;
 }
 
+// Pages of P tokens that hold `tokens` >= 0 (tokens + P may pass 32 bits).
+__device__ __forceinline__ int page_count(int tokens, int P) { return tokens / P + (tokens % P != 0); }
+
 // ---------------------------------------------------------------- dtypes
 template <int DT> struct Dt;
 template <> struct Dt<PALU_F32> {
