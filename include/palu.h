@@ -452,7 +452,7 @@ palu_status palu_select_pages(const palu_config* cfg, int batch, int num_queries
  * value product as the sum of three 16-bit numbers, as exact as in float32.  Keys
  * are rotated with sines and cosines that are off by at most 2^-21 (2^-23 on the
  * CUDA-core kernel).
- * num_splits (0 = automatic) splits the lists of the CUDA-core kernel; the
+ * num_splits (0 = automatic) splits the lists of the CUDA-core kernel, 4096 at most; the
  * tensor-core kernels deal all listed pages of a head group out in equal shares and
  * take any value.  ranks_k / ranks_v as in the ranked calls.
  * batch·num_queries <= 65535, list_len <= 2^24 (PALU_ERR_UNSUPPORTED above). */

@@ -331,6 +331,13 @@ size_t decode_workspace(const Layer& L, int batch, int Q, int max_pages, int num
   return kStatusBytes + part + fq;
 }
 
+// The split count of a sparse step on the CUDA-core kernel: its merge keeps a weight per split in shared
+// memory, so more than these are not made.
+int sparse_S(const palu_config* c, int units, int list_len, int num_splits) {
+  constexpr int kMostSplits = 4096;
+  return run_S(c, 1, units, list_len, num_splits < kMostSplits ? num_splits : kMostSplits);
+}
+
 // The walk of a sparse step's tensor-core launches (pages_walk.cuh): queries per
 // launch, CTAs per block column, and the workspace one launch and its combine use.
 struct WalkPlan {
@@ -369,8 +376,8 @@ size_t pages_workspace(const Layer& L, int batch, int Q, int list_len, int num_s
     const palu_config cc = set_cfg(L, c);
     const int kind = kernel_kind(&cc);
     const size_t n =
-        kind == 1 ? align256((size_t)batch * Q * cc.num_heads *
-                             run_S(&cc, kind, batch * Q, list_len, num_splits) * (cc.rank_v + 2) * sizeof(float))
+        kind == 1 ? align256((size_t)batch * Q * cc.num_heads * sparse_S(&cc, batch * Q, list_len, num_splits) *
+                             (cc.rank_v + 2) * sizeof(float))
                   : walk_plan(&cc, kind, batch, Q, list_len).total();
     if (n > most) most = n;
   }
@@ -581,7 +588,8 @@ palu_status decode_layer(const Layer& L, int batch, int Q, const void* q, const 
   for (int c = 0; c < L.nset; ++c) {
     const palu_config cc = set_cfg(L, c);
     const int kind = kernel_kind(&cc);
-    a.S = run_S(&cc, kind, a.batch, walk, num_splits, sparse ? 1 : pass_queries(kind, Q));
+    a.S = sparse ? sparse_S(&cc, a.batch, walk, num_splits)
+                 : run_S(&cc, kind, a.batch, walk, num_splits, pass_queries(kind, Q));
     a.r_k = cc.rank_k;
     a.r_v = cc.rank_v;
     a.k_row = palu::latent_row_bytes(a.lat, a.r_k);

@@ -539,3 +539,11 @@ def test_more_queries_than_one_launch_walks(name, Q, keep, batch):
     q, q_pos = queries(case, Q)
     lists = pick_lists(case, Q, min(keep, 3))
     compare(case, *run(case, build_pools(case), q, q_pos, lists, keep), q, q_pos, lists, uniform(case))
+
+
+@pytest.mark.parametrize("name", ["tiny_f32", "bf16"])
+def test_more_splits_than_a_merge_holds(name):
+    case = make_decode_case(CASES[name][0], [700])
+    q, q_pos = queries(case, 1)
+    lists = [[[[0, 2, 5]] * case.w.groups]]
+    compare(case, *run(case, build_pools(case), q, q_pos, lists, 20000, 20000), q, q_pos, lists, uniform(case))
