@@ -556,9 +556,11 @@ cudaError_t launch_tc(const BoundsArgs& all, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // one CTA per SM, the same number for every (group, head pair), each with its B_k resident
   const int combos = all.gm.n * (all.gs / 2);
-  for (int b0 = 0; b0 < all.batch; b0 += kMaxSeqs) {
+  // sequences of one launch: their pages, and a step of the grid past them, are counted in 32 bits
+  const int most_seqs = (INT32_MAX - 256) / all.max_pages < kMaxSeqs ? (INT32_MAX - 256) / all.max_pages : kMaxSeqs;
+  for (int b0 = 0; b0 < all.batch; b0 += most_seqs) {
     BoundsArgs a = all;
-    a.batch = all.batch - b0 < kMaxSeqs ? all.batch - b0 : kMaxSeqs;
+    a.batch = all.batch - b0 < most_seqs ? all.batch - b0 : most_seqs;
     a.page_table += (size_t)b0 * a.max_pages;
     a.seq_lens += b0;
     if (a.first != nullptr) a.first += b0;

@@ -229,3 +229,22 @@ def test_a_key_rank_past_256(ranks_k):
         return list(zip(zk, Bk))
 
     check(case, run(case.cfg, case, build_ranked_pools(case), case.B_k, ranks_k=ranks_k), keys)
+
+
+def test_a_wide_table_is_counted_in_several_launches():
+    """160 sequences of up to 2^24 - 1 pages: together more pages than 32 bits count, of which a few are rebuilt."""
+    w = dataclasses.replace(w7b(), num_heads=4, rank_k=64, rank_v=128)
+    wide = 2 ** 24 - 1
+    case = make_decode_case(w, [130] * 160)
+    narrow = torch.from_numpy(case.page_table).cuda()
+    table = torch.full((160, wide), -1, dtype=torch.int32, device="cuda")
+    table[:, :2] = narrow
+    launches = P.palu_kernel_launches()
+    bounds = torch.full((case.num_pages, 1, 2, 512), FILL, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(P.palu_page_bounds_workspace_size(case.cfg, 160, wide), dtype=torch.uint8, device="cuda")
+    pools = build_pools(case)
+    P.palu_page_bounds(case.cfg, None, pools["zk"], None, None, table, torch.full((160,), 130, dtype=torch.int32, device="cuda"),
+                       case.num_pages, case.B_k.cuda(), bounds, ws)
+    torch.cuda.synchronize()
+    assert P.palu_get_device_status(ws)[0] == 0 and P.palu_kernel_launches() == launches + 2
+    check(case, bounds, uniform(case))
