@@ -241,3 +241,22 @@ def test_query_entries_that_cancel_under_rotation(name, far):
             side = int(rng.integers(0, 2))
             box[side, f] = far if side else -far
     check(c, 2, 0, 0, scores=False)
+
+
+@pytest.mark.parametrize("name,pages,levels", [("one_head_d8", 32768, 0), ("one_head_d8", 32768, 40), ("widest", 32768, 50)])
+def test_the_largest_tables(name, pages, levels):
+    """As many pages as the cut keeps keys of; all but a few distinct boxes have equal scores among them."""
+    w = SHAPES[name] if name in SHAPES else dataclasses.replace(W7B, num_heads=64, group_size=64, page_size=128)
+    real = 64 if levels else pages
+    c = make(w, [PAGE * real], seed=31, levels=levels)
+    g = torch.Generator().manual_seed(32)
+    if levels:
+        c["table"] = torch.randint(0, c["pages"], (1, pages), generator=g).to(torch.int32)
+        c["lens"] = [PAGE * pages - 5]
+        c["q_pos"][:] = c["lens"][0] - 1
+    if name == "widest":                # (one head's oracle: the others have no part in the score)
+        c["q"][:, :, 1:] = 0
+        c["bounds"][..., 128:] = 0
+        c["q"][:, :, 0] *= 8
+    check(c, 777, scores=False)
+    check(c, 5, 0, 0, scores=False)

@@ -164,3 +164,16 @@ def test_captured_call_follows_its_inputs():
             ref, a = S.verify_drafts(d["target"][b].double().numpy(), d["draft"][b].double().numpy(),
                                      d["tokens"][b].numpy(), int(d["lens"][b]), d["ua"][b].numpy(), float(d["us"][b]))
             assert (out[b].tolist(), int(acc[b])) == (ref, a)
+
+
+@pytest.mark.parametrize("dtype,batch,V", [("bf16", 2, 1000003), ("f32", 1, 2 ** 21)])
+def test_large_vocabularies(dtype, batch, V):
+    """More groups than the drawing CTA keeps sums of."""
+    c = make(batch, 2, V, dtype, seed=20)
+    for u in (0.001, 0.7, 0.99999):
+        c["us"][:] = u
+        check(c, twice=False)
+
+
+def test_the_largest_batch():
+    check(make(8192, 1, 300, "f32", seed=21), twice=False)
