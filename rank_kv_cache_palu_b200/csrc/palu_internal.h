@@ -2,6 +2,7 @@
 // launchers.  Host-side only; not part of the public ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -153,11 +154,16 @@ cudaError_t allow_shared(K* kernel, size_t bytes, size_t fixed = 0) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(227 * 1024 - fixed));
 }
 
-// Makes the current device's context current to the calling host thread.  The driver's tensor-map encoder
-// fails without one, and a thread whose first CUDA call is one of this library's has none yet.
-inline void bind_context() {
-  int device = 0;
-  if (cudaGetDevice(&device) == cudaSuccess) cudaSetDevice(device);
+// Whether a tensor map could be encoded.  The encoder needs a context current to the calling host thread, and
+// a thread whose first CUDA call is one of this library's has none yet: it gets the current device's.
+template <class F>
+bool encoded(F encode) {
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int device = 0;
+    if (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = encode();
+  }
+  return r == CUDA_SUCCESS;
 }
 
 // Counts kernel launches (palu_kernel_launches); call once per launch.
