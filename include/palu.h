@@ -327,8 +327,8 @@ palu_status palu_decode_attn_noalloc(const palu_config* cfg, int batch, const vo
  *   taken      [batch] int32 or NULL (written): num_new[b], or 0 where refused
  * Pages come off the top of the stack in (sequence, page) order.  A sequence
  * gets all the pages it needs or none: it is refused (its length and table stay)
- * when the needs of the sequences up to it exceed num_free.  A page belongs to
- * one sequence (one that two share would be given back twice).  Pages given back
+ * when it needs pages and the needs of the sequences up to it exceed num_free.  A
+ * page belongs to one sequence (one that two share would be given back twice).  Pages given back
  * go on top of what is left, the last in (sequence, page) order first, so
  * dropping what the last call appended restores the stack; they serve the next
  * call, not this one.

@@ -295,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, 2) plan_kernel(const PlanArgs a) {
   if (tid == 0) *a.num_free = (int)min(left + given, (long long)a.num_pages);
 }
 
-// Rows up to which each has a thread of its own (a CTA on every SM): 256 rows 5.8 us against 7.1
-// with four a thread; 500k rows 12.0 us with four a thread.
+// Rows up to which each has a thread of its own, as many as fit a CTA on every SM.  One a thread
+// against four, 16 sequences: 20k rows 8.2 to 9.5 us, 75k 8.6 to 9.9, 90k 9.9 to 9.7, 200k 12.4 to
+// 10.1, 500k 20.2 to 12.2; 256 sequences: 75k 9.5 to 10.9, 90k 10.9 both, 200k 13.2 to 10.9.
 constexpr int kSmall = 148 * kThreads;
 
 template <int ROWS>
