@@ -13,8 +13,8 @@
 //   - the softmax weights reach the value MMA as sums of three 16-bit numbers
 //     (split_weight), rows p, 4 + p and 8 + p of its 16.
 // Bound by the latents' bytes from HBM: 14 queries x 64 pages in each of 8 groups (r 256/128,
-// f16, 0.71 GB) 126 us with the fold and the merge, 0.86 of the measured copy bandwidth; this
-// kernel alone 115 us, 0.94.
+// f16, 0.71 GB) 128 us with the fold and the merge, 0.84 of the measured copy bandwidth; this
+// kernel alone 114 us, 0.95.
 #include <cuda.h>
 #include <math.h>
 

@@ -18,10 +18,10 @@
 //     its operands went through lane registers and every group of MMAs took 700 to 850 cycles
 //     to issue, which set the tile period (16 queries x 32 pages bf16: 170 us; with descriptors
 //     made by one addition 163; converged 143.  int4, 32 queries x 16 pages: 266, 258, 245).
-// Measured in the 7B shape, r 256/128 bf16, 16 queries x 32 pages in each of 8 groups: 138 to 144 us
-// with the merge (0.96 PFLOP/s of key and value products or more, 0.58 of the burst peak), bound as the dense kernel by
-// the coupling of the operand rings to the TMEM slots; one query x 16 pages 17.6 us.  int4, r 256/256, 8 sequences x 4 queries x
-// 16 pages: 230 us, bound by the conversion of codes.
+// Measured in the 7B shape, r 256/128 bf16, 16 queries x 32 pages in each of 8 groups: 139 to 149 us by the GPU
+// with the merge (0.93 PFLOP/s of key and value products or more, 0.56 of the burst peak), bound as the dense kernel by
+// the coupling of the operand rings to the TMEM slots; one query x 16 pages 18.1 us.  int4, r 256/256, 8 sequences x 4 queries x
+// 16 pages: 231 to 236 us, bound by the conversion of codes.
 #pragma once
 
 #include "decode_tc_kernel.cuh"

@@ -23,8 +23,8 @@
 // list in a hundred with random boxes; every page where E is not finite).
 //
 // Bound by the stream of bounds for many lists and by latency for few.  Measured in the 7B
-// shape (8 groups, width 512, bf16, one query): 14 sequences x 410 to 512 pages 30.8 us (0.1 GB,
-// 3.4 TB/s with start and cut, which take 10 us of it), one sequence x 512 pages 11.2 us.
+// shape (8 groups, width 512, bf16, one query): 14 sequences x 410 to 512 pages 30.0 us (0.1 GB,
+// 3.5 TB/s with start and cut, which take 10 us of it), one sequence x 512 pages 11.1 us.
 //
 // The last CTA of a list (a ticket) cuts it: scores become
 // order-preserving keys; a histogram over the 8 bits below the highest bit in which

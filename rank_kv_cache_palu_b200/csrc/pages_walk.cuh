@@ -31,7 +31,7 @@ __device__ __forceinline__ int tile_rows(int info) { return info & kTileRows; }
 // What a partial page's unused rows are filled with in shared memory: the page's own
 // bytes there may be anything (NaN included), and a weight of 0 does not silence a NaN.
 // (A loop over the valid rows on CUDA cores, the alternative, took the no-RoPE step of
-// 16 queries x 64 pages from 143 to 221 us.)
+// 14 queries x 64 pages from 143 to 221 us.)
 __device__ uint4 g_zero_rows[128 * 128 / 16];
 
 // Fills tiles[] of this CTA (block (x, y) of gridDim.x CTAs per column) for model
